@@ -25,6 +25,7 @@ STATUS_NAN_SCORE = 2
 STATUS_PREFILL_PENDING_OVERFLOW = 4
 STATUS_BAD_COUNTERS = 8
 STATUS_TIMEOUT = 16
+STATUS_BAD_LENGTH = 32
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
@@ -45,6 +46,16 @@ class _Layout(ctypes.Structure):
         "total_bytes", "ring_k", "ring_v", "bank_k", "bank_v", "bank_score",
         "pend_k", "pend_v", "pend_score", "counters", "tickets", "status",
         "ring_k_exp", "ring_v_exp", "bank_k_exp", "bank_v_exp", "pend_k_exp", "pend_v_exp")]
+
+
+class _GdnConfig(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_layers", ctypes.c_int32), ("n_k_heads", ctypes.c_int32),
+                ("n_v_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("conv_width", ctypes.c_int32),
+                ("qk_l2norm", ctypes.c_int32), ("l2_eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class _GdnLayout(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_uint64) for n in ("total_bytes", "conv", "delta", "status")]
 
 
 def _load():
@@ -73,13 +84,29 @@ def _load():
     lib.rma_get_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.rma_state_quantize.argtypes = [vp, vp, vp]
     lib.rma_set_decode_overlap.argtypes = [vp, i32]
+    i64, f32, size = ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+    gcfgp = ctypes.POINTER(_GdnConfig)
+    lib.rma_qk_norm_rope.argtypes = [vp, i32, i32, vp, i64, vp, i64, vp, vp, f32, vp, i32, i32, vp, vp, vp, vp]
+    lib.rma_gdn_state_bytes.argtypes = [gcfgp]
+    lib.rma_gdn_state_bytes.restype = size
+    lib.rma_gdn_state_alloc.argtypes = [gcfgp, vp, size, vp, ctypes.POINTER(vp)]
+    lib.rma_gdn_state_layout.argtypes = [vp, ctypes.POINTER(_GdnLayout)]
+    lib.rma_gdn_state_free.argtypes = [vp]
+    lib.rma_gdn_state_free.restype = None
+    lib.rma_gdn_workspace_bytes.argtypes = [vp, i32, ctypes.POINTER(size)]
+    lib.rma_gdn_conv.argtypes = [vp, i32, i32, vp, i64, vp, vp, vp, vp, vp]
+    lib.rma_gdn_decode_step.argtypes = [vp, i32, vp, vp, vp, i64, vp, vp, vp, vp]
+    lib.rma_gdn_prefill.argtypes = [vp, i32, i32, vp, vp, vp, i64, vp, vp, vp, vp, vp, size, vp]
+    lib.rma_gdn_get_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     lib.rma_strerror.argtypes = [i32]
     lib.rma_strerror.restype = ctypes.c_char_p
     lib.rma_last_error.argtypes = []
     lib.rma_last_error.restype = ctypes.c_char_p
     for f in ("rma_state_alloc", "rma_state_layout", "rma_workspace_bytes", "rma_set_decode_splits",
               "rma_decode_step", "rma_decode_step_noalloc", "rma_admit", "rma_prefill_block", "rma_get_status",
-              "rma_state_quantize", "rma_set_decode_overlap"):
+              "rma_state_quantize", "rma_set_decode_overlap", "rma_qk_norm_rope", "rma_gdn_state_alloc",
+              "rma_gdn_state_layout", "rma_gdn_workspace_bytes", "rma_gdn_conv", "rma_gdn_decode_step",
+              "rma_gdn_prefill", "rma_gdn_get_status"):
         getattr(lib, f).restype = ctypes.c_int
     return lib
 
@@ -319,3 +346,7 @@ def get_status(state: State, stream=None) -> int:
     flags = ctypes.c_uint32()
     _check(lib.rma_get_status(state.handle, _stream_handle(stream), ctypes.byref(flags)), "rma_get_status")
     return int(flags.value)
+
+
+from .layers import (GdnConfig, GdnState, gdn_conv, gdn_decode_step, gdn_get_status, gdn_prefill,  # noqa: E402,F401
+                     gdn_state_bytes, qk_norm_rope)

@@ -14,7 +14,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librma.so")
-SOURCES = ["rma_api.cu", "rma_decode.cu", "rma_admit.cu", "rma_prefill.cu"]
+SOURCES = ["rma_api.cu", "rma_decode.cu", "rma_admit.cu", "rma_prefill.cu",
+           "rma_rope.cu", "rma_gdn.cu", "rma_gdn_api.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

@@ -222,6 +222,35 @@ int check_layer(const State* s, int layer) {
 }
 
 }  // namespace
+
+int api_fail(int code, const char* why) noexcept {
+    try {
+        g_last_error = why;
+    } catch (...) {
+        g_last_error.clear();   // no memory for the text; the code still says what failed
+    }
+    return code;
+}
+
+int api_cuda_fail(cudaError_t e, const char* what) noexcept {
+    char text[256];
+    std::snprintf(text, sizeof text, "%s: %s", what, cudaGetErrorString(e));
+    return api_fail(RMA_ERR_CUDA, text);
+}
+
+void api_note_launch(cudaStream_t stream) noexcept {
+    try {
+        note_other_launch(stream);
+    } catch (...) {
+        // the record could not be written: forget every stream's, which only makes decode calls wait
+        try {
+            std::lock_guard<std::mutex> lock(g_launch_mu);
+            g_last_launch.clear();
+        } catch (...) {
+        }
+    }
+}
+
 }  // namespace rma
 
 using namespace rma;
@@ -257,6 +286,7 @@ int rma_state_alloc(const rma_config* cfg, void* dev_buf, size_t dev_bytes, void
     s->bank_splits_override = 0;
     s->sm_count = sms;
     s->decode_overlap = 0;
+    s->device = dev;
     e = cudaMemsetAsync(s->base + L.counters, 0, L.total_bytes - L.counters, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) {
         delete s;

@@ -1,0 +1,235 @@
+// The gated-delta-rule layers: the short convolution, and the delta rule token by token.
+#include "rma_gdn.cuh"
+
+namespace rma {
+namespace {
+
+// ---------------------------------------------------------------------------
+// rma_gdn_conv: z[t] = bias + sum_j w[j] x[t - 3 + j], out = silu(z), and the three-row state.
+//
+// Memory bound: 2 bytes read and 2 written per (token, channel), the state's 12 bytes per channel
+// and sequence.  A thread keeps 8 channels' weights in registers (16-byte loads and stores of the
+// activations) and walks down a tile of tokens with the last three rows in registers, so a row is
+// read once per tile plus three rows of overlap; single tokens walk over sequences instead, so
+// that the weights (16 bytes a channel, more than the activations) are fetched once per several.
+// The state is read by the first tile only and written by the same threads, after their reads.
+// ---------------------------------------------------------------------------
+constexpr int kConvThreads = 128;
+constexpr int kConvVec = 8;
+
+__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
+    const float2 p0 = unpack_bf16(r.x), p1 = unpack_bf16(r.y), p2 = unpack_bf16(r.z), p3 = unpack_bf16(r.w);
+    x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
+    x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
+}
+
+// z / (1 + exp(-z)); exp overflows to infinity below -88, where the quotient is -0
+__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+
+__global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_constant__ ConvArgs a, int tile, int tiles,
+                                                                int seqs, int cblocks) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int cb = blockIdx.x % cblocks;
+    const int tl = (blockIdx.x / cblocks) % tiles;
+    const int b0 = (blockIdx.x / cblocks / tiles) * seqs;
+    const int c = (cb * kConvThreads + threadIdx.x) * kConvVec;
+    if (c >= a.C) return;
+    const int t0 = tl * tile;
+    float w[8][4], bias[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.w) + c + i);
+        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+        bias[i] = 0.f;
+    }
+    if (a.bias) {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(a.bias + c)), v = __ldg(reinterpret_cast<const float4*>(a.bias + c) + 1);
+        bias[0] = u.x; bias[1] = u.y; bias[2] = u.z; bias[3] = u.w;
+        bias[4] = v.x; bias[5] = v.y; bias[6] = v.z; bias[7] = v.w;
+    }
+    for (int b = b0; b < min(b0 + seqs, a.B); ++b) {
+        const int len = seq_len(a.lens, b, a.n, a.status, tl == 0 && cb == 0 && threadIdx.x == 0);
+        if (t0 >= len) continue;
+        const uint16_t* x = a.x + (int64_t)b * a.n * a.x_stride + c;
+        uint16_t* st = a.state + (int64_t)b * 3 * a.C + c;
+        uint16_t* out = a.out + (int64_t)b * a.n * a.C + c;
+        auto row = [&](int t) { return *reinterpret_cast<const uint4*>(x + (int64_t)t * a.x_stride); };
+        uint4 h[3];
+        if (t0 == 0) {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) h[j] = *reinterpret_cast<const uint4*>(st + (int64_t)j * a.C);
+            // the last three rows of (state, x): row len + j of the two in sequence
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                const int i = len + j;
+                const uint4 v = i >= 3 ? row(i - 3) : (i == 1 ? h[1] : h[2]);
+                *reinterpret_cast<uint4*>(st + (int64_t)j * a.C) = v;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 3; ++j) h[j] = row(t0 - 3 + j);   // tile >= 3: never before row 0
+        }
+        float p0[8], p1[8], p2[8];
+        unpack8(h[0], p0);
+        unpack8(h[1], p1);
+        unpack8(h[2], p2);
+        const int end = min(t0 + tile, len);
+#pragma unroll 4
+        for (int t = t0; t < end; ++t) {
+            float p3[8], y[8];
+            unpack8(row(t), p3);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float z = fmaf(w[i][0], p0[i], bias[i]);
+                z = fmaf(w[i][1], p1[i], z);
+                z = fmaf(w[i][2], p2[i], z);
+                z = fmaf(w[i][3], p3[i], z);
+                y[i] = silu(z);
+                p0[i] = p1[i];
+                p1[i] = p2[i];
+                p2[i] = p3[i];
+            }
+            *reinterpret_cast<uint4*>(out + (int64_t)t * a.C) =
+                make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// The delta rule token by token (rma_gdn_decode_step, and prefill blocks too short for chunks).
+//
+//   S <- e^g S;  u = beta (v - S^T k);  S <- S + k u^T;  o = S^T q = (e^g S)^T q + (k.q) u,
+//
+// so one pass over the decayed state gives both products and the update follows in registers: the
+// state is read once and written once, which is the bound (64 KiB each way per value head).  A CTA
+// holds SLICE value columns of one (sequence, value head), all 128 key rows, in registers; columns
+// never meet, so a small batch splits a head over 4 CTAs.  Sums over the key rows go through
+// shuffles and one exchange in shared memory.  Everything is FP32.
+// ---------------------------------------------------------------------------
+constexpr int kRecThreads = 256;
+constexpr int kRecWarps = kRecThreads / 32;
+
+template <int SLICE>
+__global__ void __launch_bounds__(kRecThreads) gdn_recurrent_kernel(const __grid_constant__ DeltaArgs a) {
+    constexpr int kLanes = SLICE / 4;                 // lanes of one key row, 4 columns each
+    constexpr int kSub = 32 / kLanes;                 // key rows of a warp at a time
+    constexpr int kRows = kGdnDim / (kRecWarps * kSub);
+    constexpr int kSlices = kGdnDim / SLICE;
+    __shared__ __align__(16) float sk[2][kGdnDim], sq[2][kGdnDim];
+    __shared__ __align__(16) float red[2][kRecWarps][2][SLICE];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x / kSlices, slice = blockIdx.x % kSlices;
+    const int b = unit / a.HV, h = unit % a.HV;
+    const int kh = h / (a.HV / a.HK);
+    const int len = seq_len(a.lens, b, a.n, a.status, h == 0 && slice == 0 && threadIdx.x == 0);
+    if (len == 0) return;
+    const int col = 4 * (lane % kLanes), sub = lane / kLanes;
+    float* S = a.state + ((int64_t)unit * kGdnDim) * kGdnDim + slice * SLICE + col;
+    float4 s[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        s[i] = *reinterpret_cast<const float4*>(S + ((i * kRecWarps + warp) * kSub + sub) * kGdnDim);
+    const float alpha = expf(a.a_log[h]), dt = a.dt_bias[h];
+
+    for (int t = 0; t < len; ++t) {
+        const int buf = t & 1;
+        const int64_t tok = (int64_t)b * a.n + t;
+        const uint16_t* x = a.qkv + tok * a.C;
+        const uint2 qr = *reinterpret_cast<const uint2*>(x + kh * kGdnDim + 4 * lane);
+        const uint2 kr = *reinterpret_cast<const uint2*>(x + (a.HK + kh) * kGdnDim + 4 * lane);
+        const uint2 vr = *reinterpret_cast<const uint2*>(x + (2 * a.HK + h) * kGdnDim + slice * SLICE + col);
+        float decay, beta;
+        gates(a.a[tok * a.ab_stride + h], a.b[tok * a.ab_stride + h], alpha, dt, decay, beta);
+        decay = expf(decay);
+        const float2 qa = unpack_bf16(qr.x), qb = unpack_bf16(qr.y), ka = unpack_bf16(kr.x), kb = unpack_bf16(kr.y);
+        float qq = qa.x * qa.x + qa.y * qa.y + qb.x * qb.x + qb.y * qb.y;
+        float kk = ka.x * ka.x + ka.y * ka.y + kb.x * kb.x + kb.y * kb.y;
+        float kq = qa.x * ka.x + qa.y * ka.y + qb.x * kb.x + qb.y * kb.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            qq += __shfl_xor_sync(0xffffffffu, qq, o);
+            kk += __shfl_xor_sync(0xffffffffu, kk, o);
+            kq += __shfl_xor_sync(0xffffffffu, kq, o);
+        }
+        const float rq = (a.l2norm ? 1.f / sqrtf(qq + a.l2_eps) : 1.f) * a.scale;
+        const float rk = a.l2norm ? 1.f / sqrtf(kk + a.l2_eps) : 1.f;
+        kq *= rq * rk;
+        if (warp == 0) *reinterpret_cast<float4*>(&sk[buf][4 * lane]) = make_float4(ka.x * rk, ka.y * rk, kb.x * rk, kb.y * rk);
+        if (warp == 1) *reinterpret_cast<float4*>(&sq[buf][4 * lane]) = make_float4(qa.x * rq, qa.y * rq, qb.x * rq, qb.y * rq);
+        __syncthreads();
+        float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = (i * kRecWarps + warp) * kSub + sub;
+            const float k = sk[buf][r], q = sq[buf][r];
+            s[i].x *= decay; s[i].y *= decay; s[i].z *= decay; s[i].w *= decay;
+            pk.x = fmaf(k, s[i].x, pk.x); pk.y = fmaf(k, s[i].y, pk.y);
+            pk.z = fmaf(k, s[i].z, pk.z); pk.w = fmaf(k, s[i].w, pk.w);
+            pq.x = fmaf(q, s[i].x, pq.x); pq.y = fmaf(q, s[i].y, pq.y);
+            pq.z = fmaf(q, s[i].z, pq.z); pq.w = fmaf(q, s[i].w, pq.w);
+        }
+#pragma unroll
+        for (int o = kLanes; o < 32; o <<= 1) {
+            pk.x += __shfl_xor_sync(0xffffffffu, pk.x, o); pk.y += __shfl_xor_sync(0xffffffffu, pk.y, o);
+            pk.z += __shfl_xor_sync(0xffffffffu, pk.z, o); pk.w += __shfl_xor_sync(0xffffffffu, pk.w, o);
+            pq.x += __shfl_xor_sync(0xffffffffu, pq.x, o); pq.y += __shfl_xor_sync(0xffffffffu, pq.y, o);
+            pq.z += __shfl_xor_sync(0xffffffffu, pq.z, o); pq.w += __shfl_xor_sync(0xffffffffu, pq.w, o);
+        }
+        if (sub == 0) {
+            *reinterpret_cast<float4*>(&red[buf][warp][0][col]) = pk;
+            *reinterpret_cast<float4*>(&red[buf][warp][1][col]) = pq;
+        }
+        __syncthreads();
+        pk = pq = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kRecWarps; ++w) {
+            const float4 x0 = *reinterpret_cast<const float4*>(&red[buf][w][0][col]);
+            const float4 x1 = *reinterpret_cast<const float4*>(&red[buf][w][1][col]);
+            pk.x += x0.x; pk.y += x0.y; pk.z += x0.z; pk.w += x0.w;
+            pq.x += x1.x; pq.y += x1.y; pq.z += x1.z; pq.w += x1.w;
+        }
+        const float2 va = unpack_bf16(vr.x), vb = unpack_bf16(vr.y);
+        const float4 u = make_float4(beta * (va.x - pk.x), beta * (va.y - pk.y), beta * (vb.x - pk.z), beta * (vb.y - pk.w));
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const float k = sk[buf][(i * kRecWarps + warp) * kSub + sub];
+            s[i].x = fmaf(k, u.x, s[i].x); s[i].y = fmaf(k, u.y, s[i].y);
+            s[i].z = fmaf(k, u.z, s[i].z); s[i].w = fmaf(k, u.w, s[i].w);
+        }
+        if (warp == 0 && sub == 0)
+            *reinterpret_cast<uint2*>(a.out + (tok * a.HV + h) * kGdnDim + slice * SLICE + col) =
+                make_uint2(pack_bf16(fmaf(kq, u.x, pq.x), fmaf(kq, u.y, pq.y)),
+                           pack_bf16(fmaf(kq, u.z, pq.z), fmaf(kq, u.w, pq.w)));
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        *reinterpret_cast<float4*>(S + ((i * kRecWarps + warp) * kSub + sub) * kGdnDim) = s[i];
+}
+
+}  // namespace
+
+cudaError_t launch_gdn_conv(const ConvArgs& a, cudaStream_t stream) {
+    const int cblocks = (a.C / kConvVec + kConvThreads - 1) / kConvThreads;
+    const int tile = a.n == 1 ? 3 : 32;
+    const int tiles = (a.n + tile - 1) / tile;
+    const int seqs = a.n == 1 ? (a.B >= 256 ? 4 : 1) : 1;
+    const int64_t grid = (int64_t)cblocks * tiles * ((a.B + seqs - 1) / seqs);
+    if (grid > 0x7fffffffll) return cudaErrorNotSupported;
+    PdlLaunch l((unsigned)grid, kConvThreads, 0, stream);
+    return cudaLaunchKernelEx(&l.cfg, gdn_conv_kernel, a, tile, tiles, seqs, cblocks);
+}
+
+cudaError_t launch_gdn_recurrent(const DeltaArgs& a, cudaStream_t stream) {
+    const int64_t units = (int64_t)a.B * a.HV;
+    if (units >= 2 * (int64_t)a.sm_count) {
+        PdlLaunch l((unsigned)units, kRecThreads, 0, stream);
+        return cudaLaunchKernelEx(&l.cfg, gdn_recurrent_kernel<128>, a);
+    }
+    PdlLaunch l((unsigned)(4 * units), kRecThreads, 0, stream);
+    return cudaLaunchKernelEx(&l.cfg, gdn_recurrent_kernel<32>, a);
+}
+
+}  // namespace rma

@@ -55,6 +55,7 @@ struct State {
     int bank_splits_override;
     int sm_count;
     int decode_overlap;    // rma_set_decode_overlap
+    int device;            // the device current at rma_state_alloc
 };
 
 // Per-call view of one layer of the state, with device pointers already
@@ -140,5 +141,76 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 // Quantise every row of `src` (BF16) into `dst` (FP8), one layer at a time; scores and counters copied.
 cudaError_t launch_quantize_layer(const LayerView& dst, const LayerView& src, cudaStream_t stream);
 size_t prefill_workspace_bytes(const rma_config& cfg, int n_tok);
+
+// ---- the layers around RMA attention (rma_qk_norm_rope, rma_gdn_*) ----
+
+struct RopeArgs {
+    const uint16_t* q;          // rows of a token contiguous, tokens q_stride apart
+    const uint16_t* k;
+    int64_t q_stride, k_stride;
+    const float* w_q;           // [D]
+    const float* w_k;
+    const double* inv_freq;     // [half]
+    const int32_t* positions;   // [B][n] or null: counters + token
+    const int32_t* counters;    // [B][G][4]
+    uint32_t* status;
+    uint16_t* q_out;            // [B][n][G*H][D]
+    uint16_t* k_out;            // [B][n][G][D]
+    int B, n, G;
+    int half;                   // rotated pairs
+    int interleaved;
+    float eps;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream);
+
+constexpr int kGdnDim = 128;     // key and value width of a delta-rule head
+constexpr int kConvWidth = 4;
+
+struct GdnState {
+    rma_gdn_config cfg;
+    rma_gdn_layout lay;
+    uint8_t* base;         // device
+    int sm_count;
+    int device;
+};
+
+struct ConvArgs {
+    const uint16_t* x;       // tokens x_stride apart
+    int64_t x_stride;
+    const float* w;          // [C][4]
+    const float* bias;       // [C] or null
+    const int32_t* lens;     // [B] or null
+    uint16_t* state;         // [B][3][C]
+    uint16_t* out;           // [B][n][C]
+    uint32_t* status;
+    int B, n, C;
+};
+cudaError_t launch_gdn_conv(const ConvArgs& a, cudaStream_t stream);
+
+struct DeltaArgs {
+    const uint16_t* qkv;     // [B][n][C]
+    const uint16_t* a;       // [B][n][HV], tokens ab_stride apart
+    const uint16_t* b;
+    int64_t ab_stride;
+    const float* a_log;      // [HV]
+    const float* dt_bias;
+    const int32_t* lens;     // [B] or null
+    float* state;            // [B][HV][128][128]
+    uint16_t* out;           // [B][n][HV][128]
+    uint8_t* ws;
+    uint32_t* status;
+    int B, n, HK, HV, C;
+    int l2norm;
+    float l2_eps, scale;
+    int sm_count;
+};
+// The token-by-token form, any n (one launch).
+cudaError_t launch_gdn_recurrent(const DeltaArgs& a, cudaStream_t stream);
+
+// Set the calling thread's error text; returns `code`.  Throws nothing.
+int api_fail(int code, const char* why) noexcept;
+int api_cuda_fail(cudaError_t e, const char* what) noexcept;
+// Tell the decode overlap rule that a launch other than a decode went to `stream`.  Throws nothing.
+void api_note_launch(cudaStream_t stream) noexcept;
 
 }  // namespace rma

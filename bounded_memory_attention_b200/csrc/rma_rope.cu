@@ -1,0 +1,129 @@
+// rma_qk_norm_rope: per-head RMS norm of queries and keys, then the position rotation.
+//
+//   y = x / sqrt(mean(x^2) + eps) * w;  for the rotated pairs (u, v) of a head:
+//   (y_u c - y_v s, y_v c + y_u s),  c, s = cos, sin of position * inv_freq[i].
+//
+// Memory bound: every value is read once and written once, 4 bytes in all.  A CTA is one token of
+// one KV group: its 4 query heads and its key, a warp each, 8 values (16 bytes) a lane; the sum of
+// squares is one warp reduction.  The group's angles are computed once per CTA, a thread each,
+// while the warps' loads are in flight.  A product of a far position and a frequency has an
+// absolute error of half an ulp of the angle, 0.008 rad at 2^18 in FP32, so the product and its
+// reduction to a fraction of a turn are in FP64; the fraction's sine and cosine then need FP32
+// only.  Pairs that lie in two lanes meet in the warp's row of shared memory.
+#include <cuda_bf16.h>
+
+#include "rma_internal.cuh"
+
+namespace rma {
+namespace {
+
+constexpr int kHeads = kQPerGroup + 1;   // of one group: its queries and its key
+constexpr int kRopeThreads = 32 * kHeads;
+
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&v);
+    return __bfloat1622float2(h);
+}
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+    __shared__ float cs[kHeadDim / 2], sn[kHeadDim / 2];
+    __shared__ __align__(16) float rows[kHeads][kHeadDim];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.x % a.G;
+    const int64_t tok = blockIdx.x / a.G;   // b n + i
+    grid_dep_wait();
+    grid_dep_launch();
+
+    const bool is_k = warp == kQPerGroup;
+    const uint16_t* src = is_k ? a.k + tok * a.k_stride + (int64_t)g * kHeadDim
+                               : a.q + tok * a.q_stride + (int64_t)(g * kQPerGroup + warp) * kHeadDim;
+    const uint4 raw = reinterpret_cast<const uint4*>(src)[lane];
+    const float4* w4 = reinterpret_cast<const float4*>(is_k ? a.w_k : a.w_q) + 2 * lane;
+    const float4 wa = __ldg(w4), wb = __ldg(w4 + 1);
+
+    if (a.half > 0) {
+        int64_t pos;
+        if (a.positions) {
+            pos = a.positions[tok];
+        } else {
+            const int64_t b = tok / a.n;
+            const int c = a.counters[(b * a.G + g) * 4];
+            if (c < 0 && threadIdx.x == 0) atomicOr(a.status, (unsigned)RMA_STATUS_BAD_COUNTERS);
+            pos = (int64_t)max(c, 0) + (tok - b * a.n);
+        }
+        for (int i = threadIdx.x; i < a.half; i += kRopeThreads) {
+            const double turns = (double)pos * (a.inv_freq[i] * 0.15915494309189533577);   // 1 / (2 pi)
+            const float f = (float)(turns - rint(turns));
+            sincospif(2.f * f, &sn[i], &cs[i]);
+        }
+    }
+
+    float x[8];
+    {
+        const float2 p0 = unpack(raw.x), p1 = unpack(raw.y), p2 = unpack(raw.z), p3 = unpack(raw.w);
+        x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
+        x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = 1.f / sqrtf(ss * (1.f / kHeadDim) + a.eps);
+    const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
+    __syncthreads();   // the angles
+
+    const int half = a.half, d0 = 8 * lane;
+    if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = 4 * lane + i;
+            if (p < half) {
+                const float u = x[2 * i], v = x[2 * i + 1], c = cs[p], s = sn[p];
+                x[2 * i] = u * c - v * s;
+                x[2 * i + 1] = v * c + u * s;
+            }
+        }
+    } else {
+        float4* row = reinterpret_cast<float4*>(rows[warp]) + 2 * lane;
+        row[0] = make_float4(x[0], x[1], x[2], x[3]);
+        row[1] = make_float4(x[4], x[5], x[6], x[7]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int d = d0 + i;
+            if (d < half) x[i] = x[i] * cs[d] - rows[warp][d + half] * sn[d];
+            else if (d < 2 * half) x[i] = x[i] * cs[d - half] + rows[warp][d - half] * sn[d - half];
+        }
+    }
+    uint16_t* dst = is_k ? a.k_out + (tok * a.G + g) * kHeadDim
+                         : a.q_out + (tok * a.G * kQPerGroup + g * kQPerGroup + warp) * kHeadDim;
+    reinterpret_cast<uint4*>(dst)[lane] =
+        make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.n * a.G), 1, 1);
+    cfg.blockDim = dim3(kRopeThreads, 1, 1);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel, a);
+}
+
+}  // namespace rma

@@ -310,6 +310,160 @@ RMA_API int rma_state_quantize(rma_state* dst, const rma_state* src, void* strea
 /* Wait for `stream`, then read the device status word into *flags and clear it. */
 RMA_API int rma_get_status(rma_state* st, void* stream, uint32_t* flags);
 
+/* ======================================================================
+ * The layers around RMA attention.
+ *
+ * rma_qk_norm_rope makes the q and k that rma_decode_step and
+ * rma_prefill_block take (which arrive normed and position-encoded).  The
+ * rma_gdn_* calls are the gated-delta-rule layers that the pages' model
+ * interleaves with RMA attention, [GDN, GDN, GDN, RMA] x 8 ([CARD]
+ * architecture list, [PRIM] memory table: a recurrent state and a short
+ * convolution state of fixed size beside the attention KV).  Same manner:
+ * caller-owned device memory, asynchronous calls that can be captured into a
+ * graph, argument errors found on the host, device conditions in a status
+ * word.  The calling thread's current device must be the one the state was
+ * laid out on (RMA_ERR_INVALID_ARG otherwise).
+ * ====================================================================== */
+
+/* Per-head RMS norm of queries and keys, then the position rotation, in one
+ * pass:
+ *   y = x / sqrt(mean(x^2) + eps) * w        (over the head's 256 values)
+ *   (y_u, y_v) -> (y_u c - y_v s, y_v c + y_u s),  c, s = cos, sin of
+ *   position * inv_freq[i],  for the pairs i of the first `rotary_dim` values:
+ *   (u, v) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved != 0;
+ *   values past rotary_dim keep y.
+ * Computed in FP32 and rounded once to BF16; the angle's product and its
+ * reduction are in FP64, so far positions keep their precision.
+ *   q          bf16 [batch][n_tok][n_groups*q_per_group][256], rows of one
+ *              token contiguous, consecutive tokens q_stride elements apart
+ *   k          bf16 [batch][n_tok][n_groups][256], consecutive tokens k_stride apart
+ *   w_q, w_k   f32  [256], shared by the heads
+ *   inv_freq   f64  [rotary_dim / 2], radians per position (NULL if rotary_dim is 0)
+ *   positions  i32  [batch][n_tok], or NULL: token i of sequence b is at pos + i,
+ *              pos the counter of (layer, b, group) in the state, which is the
+ *              position that the next rma_decode_step or rma_prefill_block of
+ *              this layer gives it.  Counters below 0 count as 0 and set
+ *              RMA_STATUS_BAD_COUNTERS.  Given positions may be any int32.
+ *   q_out      bf16 [batch][n_tok][n_groups*q_per_group][256]   (written)
+ *   k_out      bf16 [batch][n_tok][n_groups][256]   (written)
+ * n_tok >= 1 and batch * n_tok <= 2^24; rotary_dim even, 0 to 256; eps >= 0 and
+ * finite; strides multiples of 8, at least a row.  q_out may be q, and k_out
+ * may be k, where the stride is a row (in place); any other overlap of an
+ * output with an input or with the other output is RMA_ERR_INVALID_ARG.
+ * q, k, w_q, w_k, q_out and k_out must be 16-byte aligned, inv_freq 8.  The
+ * state is only read (and its status word set); its kv_format does not matter. */
+RMA_API int rma_qk_norm_rope(rma_state* st, int layer, int n_tok,
+                     const uint16_t* q, int64_t q_stride, const uint16_t* k, int64_t k_stride,
+                     const float* w_q, const float* w_k, float eps,
+                     const double* inv_freq, int rotary_dim, int interleaved, const int32_t* positions,
+                     uint16_t* q_out, uint16_t* k_out, void* stream);
+
+/* A length in `lens` was outside [0, n_tok]; it was clamped and the call went on. */
+#define RMA_STATUS_BAD_LENGTH  32u
+
+/* Dimensions of the gated-delta-rule layers.  A projected row holds
+ * C = (2 n_k_heads + n_v_heads) * head_dim channels: queries, keys, values.
+ * Value head h uses query and key head h / (n_v_heads / n_k_heads).  The
+ * library implements head_dim == 128 and conv_width == 4
+ * (RMA_ERR_UNSUPPORTED otherwise), any n_k_heads >= 1 and any multiple of it
+ * as n_v_heads, batch * n_v_heads <= 2^22, C <= 2^20. */
+typedef struct rma_gdn_config {
+    int32_t batch;       /* independent sequences */
+    int32_t n_layers;    /* gated-delta-rule layers (24 in the pages' model) */
+    int32_t n_k_heads;   /* query and key heads (16) */
+    int32_t n_v_heads;   /* value heads, each with its own state (32) */
+    int32_t head_dim;    /* 128 */
+    int32_t conv_width;  /* taps of the short convolution (4) */
+    int32_t qk_l2norm;   /* 1: q and k are divided by sqrt(sum x^2 + l2_eps) first; 0: taken as they are */
+    float   l2_eps;      /* >= 0 */
+    float   scale;       /* of the output, 1/sqrt(head_dim) */
+} rma_gdn_config;
+
+/* Byte offsets, from the start of the caller's state buffer (each a multiple of 256):
+ *   conv    bf16 [n_layers][batch][3][C]      the last three raw input rows, oldest first
+ *   delta   f32  [n_layers][batch][n_v_heads][128 (key)][128 (value)]
+ *   status  u32  one word (RMA_STATUS_* bits)
+ * A sequence starts from zeros.  A caller may read and write both arrays
+ * directly (a new sequence in a batch slot, a checkpoint) while no call is in
+ * flight. */
+typedef struct rma_gdn_layout {
+    uint64_t total_bytes;
+    uint64_t conv, delta, status;
+} rma_gdn_layout;
+
+typedef struct rma_gdn_state rma_gdn_state;   /* opaque host handle; the device memory is the caller's */
+
+/* Bytes of device memory the state needs for cfg, or 0 if cfg is invalid. */
+RMA_API size_t rma_gdn_state_bytes(const rma_gdn_config* cfg);
+
+/* Lay the state out over dev_buf (device memory, 256-byte aligned, at least
+ * rma_gdn_state_bytes(cfg) bytes, owned by the caller and kept alive until
+ * rma_gdn_state_free) and zero all of it on `stream`. */
+RMA_API int rma_gdn_state_alloc(const rma_gdn_config* cfg, void* dev_buf, size_t dev_bytes, void* stream,
+                                rma_gdn_state** out);
+
+/* Copy the layout of st into *out. */
+RMA_API int rma_gdn_state_layout(const rma_gdn_state* st, rma_gdn_layout* out);
+
+/* Release the host handle (not the caller's device buffer).  NULL is a no-op. */
+RMA_API void rma_gdn_state_free(rma_gdn_state* st);
+
+/* Workspace (device scratch, 256-byte aligned) that rma_gdn_prefill needs for
+ * n_tok tokens per sequence.  The caller owns it; its contents need not be
+ * preserved between calls, but two calls that can overlap on the GPU (other
+ * streams, or graphs replayed at once) need two workspaces. */
+RMA_API int rma_gdn_workspace_bytes(const rma_gdn_state* st, int n_tok, size_t* out);
+
+/* The short causal depthwise convolution with SiLU at layer `layer`, for one
+ * token or many:
+ *   z[t][c] = bias[c] + sum_j w[c][j] x[t - 3 + j][c];  out = z / (1 + exp(-z)),
+ * the rows before the first from the layer's conv state, which then takes the
+ * last three rows of (old state, x).  FP32 sums, rounded once to BF16.
+ *   x     bf16 [batch][n_tok][C], consecutive tokens x_stride elements apart
+ *   w     f32  [C][4];  bias f32 [C] or NULL
+ *   lens  i32  [batch] or NULL: sequence b has lens[b] tokens, 0 to n_tok (NULL:
+ *         all n_tok).  Rows past them are neither read nor written, and a
+ *         sequence of length 0 keeps its state.
+ *   out   bf16 [batch][n_tok][C]   (written; must not overlap x)
+ * n_tok >= 1 and batch * n_tok <= 2^24; x_stride a multiple of 8, at least C;
+ * x, w, bias and out 16-byte aligned. */
+RMA_API int rma_gdn_conv(rma_gdn_state* st, int layer, int n_tok, const uint16_t* x, int64_t x_stride,
+                 const float* w, const float* bias, const int32_t* lens, uint16_t* out, void* stream);
+
+/* One token of the gated delta rule for every sequence at layer `layer`; per
+ * value head, with state S (key x value):
+ *   S <- exp(g) S;  u = beta (v - S^T k);  S <- S + k u^T;  out = scale S^T q,
+ *   g = -exp(a_log) softplus(a + dt_bias),  beta = 1 / (1 + exp(-b)),
+ * q and k first divided by sqrt(sum x^2 + l2_eps) if the state's qk_l2norm is
+ * set.  All arithmetic and the state in FP32, the output rounded once.
+ *   qkv      bf16 [batch][C]   (as rma_gdn_conv writes it: q heads, k heads, v heads)
+ *   a, b     bf16 [batch][n_v_heads], consecutive sequences ab_stride elements apart
+ *            (+inf and -inf are allowed: forget all, forget nothing; beta 1, 0)
+ *   a_log, dt_bias  f32 [n_v_heads], finite
+ *   out      bf16 [batch][n_v_heads][128]   (written; must not overlap an input)
+ * qkv and out 16-byte aligned; ab_stride >= n_v_heads. */
+RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qkv,
+                        const uint16_t* a, const uint16_t* b, int64_t ab_stride,
+                        const float* a_log, const float* dt_bias, uint16_t* out, void* stream);
+
+/* The same recurrence over n_tok tokens per sequence, from the state the
+ * sequence is in, which then stands after its last token.
+ *   qkv      bf16 [batch][n_tok][C];  a, b  bf16 [batch][n_tok][n_v_heads],
+ *            consecutive tokens ab_stride elements apart
+ *   lens     i32  [batch] or NULL, as in rma_gdn_conv
+ *   out      bf16 [batch][n_tok][n_v_heads][128]   (written; must not overlap an input)
+ *   ws       workspace of rma_gdn_workspace_bytes(st, n_tok) bytes
+ * n_tok >= 1 and batch * n_tok <= 2^24.  qkv of the tokens inside the lengths
+ * must be finite: a NaN or infinity there spoils its sequence's outputs from up
+ * to 63 tokens before it on, and the state. */
+RMA_API int rma_gdn_prefill(rma_gdn_state* st, int layer, int n_tok, const uint16_t* qkv,
+                    const uint16_t* a, const uint16_t* b, int64_t ab_stride,
+                    const float* a_log, const float* dt_bias, const int32_t* lens, uint16_t* out,
+                    void* ws, size_t ws_bytes, void* stream);
+
+/* Wait for `stream`, then read the GDN state's status word into *flags and clear it. */
+RMA_API int rma_gdn_get_status(rma_gdn_state* st, void* stream, uint32_t* flags);
+
 /* Text for a return code. */
 RMA_API const char* rma_strerror(int code);
 

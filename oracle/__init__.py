@@ -10,3 +10,4 @@ from .rma_oracle import (Config, State, new_state, state_from_arrays, copy_state
                          STATUS_PENDING_OVERFLOW, STATUS_NAN_SCORE, STATUS_PREFILL_PENDING_OVERFLOW, admit_plan)
 from .rma_oracle_fp8 import (Fp8State, e4m3_to_f64, f32_to_e4m3, row_exponent, quantize_rows, dequantize_rows,
                              quantize_state, fp8_state_from_arrays, decode_step_fp8, admit_fp8)
+from .layers_oracle import norm_rope, conv_silu, delta_gates, delta_rule

@@ -176,3 +176,23 @@ def aligned_ramp(lead_shape, n_rows: int, head_dim: int, seed: int, lo: float, h
     z = torch.randn(tuple(lead_shape) + (n_rows, head_dim), generator=_gen(int(seed) + 1, device),
                     device=device, dtype=torch.float32)
     return (c[:, None] * u + noise * z).to(torch.bfloat16)
+
+
+def gdn_inputs(batch: int, n_tok: int, n_k_heads: int, n_v_heads: int, seed: int, device="cpu",
+               head_dim: int = 128, mean: float = 0.25) -> dict:
+    """One gated-delta-rule layer's inputs: qkv [B, n, C] bf16 ~ N(mean, 1) (keys share a direction, as
+    they do after an activation), a, b [B, n, HV] bf16 ~ N(0, 1), a_log [HV] f32 of rates 1 to 16,
+    dt_bias [HV] f32 for time steps 0.001 to 0.1, and a state [B, HV, D, D] f32 ~ N(0, 0.01)."""
+    s = int(seed) * 16 + 7
+    C = (2 * n_k_heads + n_v_heads) * head_dim
+    g = _gen(s + 4, device)
+    rate = 1.0 + 15.0 * torch.rand((n_v_heads,), generator=g, device=device)
+    step = 0.001 * 100.0 ** torch.rand((n_v_heads,), generator=g, device=device)
+    return {
+        "qkv": (bf16_normal((batch, n_tok, C), s, device).float() + mean).to(torch.bfloat16),
+        "a": bf16_normal((batch, n_tok, n_v_heads), s + 1, device),
+        "b": bf16_normal((batch, n_tok, n_v_heads), s + 2, device),
+        "a_log": torch.log(rate),
+        "dt_bias": step + torch.log(-torch.expm1(-step)),
+        "state": f32_normal((batch, n_v_heads, head_dim, head_dim), s + 3, device, std=0.1),
+    }
