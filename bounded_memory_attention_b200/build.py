@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "librma.so")
 SOURCES = ["rma_api.cu", "rma_decode.cu", "rma_admit.cu", "rma_prefill.cu",
-           "rma_rope.cu", "rma_gdn.cu", "rma_gdn_api.cu"]
+           "rma_rope.cu", "rma_gdn.cu", "rma_gdn_prefill.cu", "rma_gdn_api.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 FLAGS = [

@@ -261,7 +261,7 @@ int rma_gdn_workspace_bytes(const rma_gdn_state* st, int n_tok, size_t* out) {
     if (!st || !out) return api_fail(RMA_ERR_INVALID_ARG, "state and out must be non-NULL");
     const int rc = check_call(as_gdn(st), 0, n_tok);
     if (rc != RMA_OK) return rc;
-    *out = 256;
+    *out = gdn_prefill_workspace_bytes(as_gdn(st)->cfg, n_tok);
     return RMA_OK;
 }
 
@@ -341,7 +341,7 @@ int rma_gdn_prefill(rma_gdn_state* st, int layer, int n_tok, const uint16_t* qkv
     rc = check_device(s->device);
     if (rc != RMA_OK) return rc;
     d.ws = static_cast<uint8_t*>(ws);
-    return launched(launch_gdn_recurrent(d, static_cast<cudaStream_t>(stream)), "launching rma_gdn_prefill", stream);
+    return launched(launch_gdn_prefill(d, static_cast<cudaStream_t>(stream)), "launching rma_gdn_prefill", stream);
 }
 
 int rma_gdn_get_status(rma_gdn_state* st, void* stream, uint32_t* flags) {

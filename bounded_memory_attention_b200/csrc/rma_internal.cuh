@@ -206,6 +206,10 @@ struct DeltaArgs {
 };
 // The token-by-token form, any n (one launch).
 cudaError_t launch_gdn_recurrent(const DeltaArgs& a, cudaStream_t stream);
+// Blocks shorter than this go token by token.
+constexpr int kGdnChunkedFrom = 8;
+cudaError_t launch_gdn_prefill(const DeltaArgs& a, cudaStream_t stream);
+size_t gdn_prefill_workspace_bytes(const rma_gdn_config& c, int n);
 
 // Set the calling thread's error text; returns `code`.  Throws nothing.
 int api_fail(int code, const char* why) noexcept;

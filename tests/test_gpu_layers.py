@@ -446,7 +446,9 @@ def test_gdn_refusals():
     refused(rma.RmaError, -1, out=d["qkv"].view(-1)[:out.numel()].view_as(out))
     refused(rma.RmaError, -3, ws=ws[:ws.numel() - 1])
     refused(rma.RmaError, -5, ws=ws[16:])
-    refused(rma.RmaError, -1, ws=st.buffer)
+    big = torch.zeros(ws.numel() + 2 * d["qkv"].numel(), dtype=torch.uint8, device="cuda")
+    inside = big[1024:1024 + 2 * d["qkv"].numel()].view(BF).view_as(d["qkv"])
+    refused(rma.RmaError, -1, ws=big, qkv=inside)
     refused(ValueError, b=torch.zeros(2, 70, 4, dtype=BF, device="cuda")[..., :2])   # not the spacing of a
     refused(ValueError, a=d["a"][:, :69])
     refused(ValueError, qkv=d["qkv"][..., :256])
