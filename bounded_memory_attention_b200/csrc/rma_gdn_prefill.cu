@@ -42,10 +42,11 @@ constexpr int kTile = kC * 128;               // 64 rows of 64 FP16: one operand
 // a (chunk, key head) block of the workspace: K columns 0-63, 64-127, Q columns 0-63, 64-127
 constexpr int kKQBytes = 4 * kTile;
 // a (chunk, value head) block: T hi, T lo, P, then FP32 scalars
-constexpr int kTPBytes = 3 * kTile + 1536;
+constexpr int kTPBytes = 3 * kTile + 1024;
 constexpr int kOffTLo = kTile, kOffP = 2 * kTile, kOffScal = 3 * kTile;
-// scalars: factors of token i in W (c1), Q S0 (c2), U' (c3), the scales of T's and P's rows, e^{G_C}
-constexpr int kC1 = 0, kC2 = 64, kC3 = 128, kTS = 192, kPS = 256, kEC = 320;
+// scalars: factors of token i in W (c1), Q S0 (c2) and U' (c3); then single values: e^{G_C}, the inverse
+// scales of T and P, and the bounds that the scan takes its scales from (see there)
+constexpr int kC1 = 0, kC2 = 64, kC3 = 128, kEC = 192, kTS = 193, kPS = 194, kBW = 196, kBT = 197, kBS = 198;
 
 // ---- powers of two ----
 __device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 0xffu) - 127; }
@@ -80,6 +81,19 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// four 8 x 8 matrices of 16-bit values, transposed: lane l's address takes column l & 7 of matrix l >> 3
+__device__ __forceinline__ void stsm4_trans(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(r0), "r"(r1),
+                 "r"(r2), "r"(r3)
+                 : "memory");
+}
+// Copy `bytes` (a multiple of 16) of shared memory to global memory, both 16-byte aligned.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(reinterpret_cast<uint64_t>(dst)),
+                 "r"(ptx::smem_u32(src)), "r"(bytes)
+                 : "memory");
+}
+
 // byte offset of 16-byte piece `piece` (8 values) of row `row` in an operand image
 __device__ __forceinline__ int piece_at(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
 
@@ -96,7 +110,9 @@ struct __align__(1024) PrepSmem {
     float Y[32][33];
     double G[kHeadsAtOnce][kC];
     float beta[kHeadsAtOnce][kC];
-    float rk[kC], rq[kC];
+    float rk[kC], rq[kC], ks[kC];   // row factors of K and Q, sums of |K|
+    float c1[kC], c3[kC], tsum[kC];
+    uint32_t pmax, tmax;            // largest |P| and |T| (float bits)
 };
 
 __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
@@ -134,14 +150,18 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
             for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const int e = scale_exponent(mx, 8);
             const float f = pow2(e), inv = pow2(-e);
-            float ss = 0.f;
+            float ss = 0.f, sa = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 x[i] *= f;
                 ss = fmaf(x[i], x[i], ss);
+                sa += fabsf(x[i]);
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int o = 8; o > 0; o >>= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                sa += __shfl_xor_sync(0xffffffffu, sa, o);
+            }
             *reinterpret_cast<uint4*>(s.kq + (2 * m + (l16 >> 3)) * kTile + piece_at(row, l16 & 7)) =
                 make_uint4(half2_bits(x[0], x[1]), half2_bits(x[2], x[3]), half2_bits(x[4], x[5]), half2_bits(x[6], x[7]));
             if (l16 == 0) {
@@ -154,7 +174,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                 }
                 if (row >= valid) r = 0.f;
                 if (m) s.rq[row] = r * a.scale;
-                else s.rk[row] = r;
+                else s.rk[row] = r, s.ks[row] = sa;
             }
         }
     }
@@ -221,12 +241,15 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
             s.beta[warp][2 * lane + 1] = bt[1];
         }
         for (int r = r0; r < min(r0 + kHeadsAtOnce, R); ++r) {
+            if (tid == 0) s.pmax = 0u;
             __syncthreads();
+            if (tid == 0) s.tmax = 0u;
             const double* G = s.G[r - r0];
             const float* beta = s.beta[r - r0];
             uint8_t* out = tp_base + (((int64_t)b * a.HV + kh * R + r) * NC + c) * kTPBytes;
             float* scal = reinterpret_cast<float*>(out + kOffScal);
             const int i0 = 16 * rb + (lane >> 2);
+            float p[32];
             if (m == 0) {
                 // A, strictly below the diagonal
 #pragma unroll
@@ -244,14 +267,20 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                             s.A[i][j] = v;
                         }
                 }
+                if (tid < kC) {
+                    const float since = __expf((float)G[tid]), until = __expf((float)(G[kC - 1] - G[tid]));
+                    scal[kC1 + tid] = s.c1[tid] = since * s.rk[tid];
+                    scal[kC2 + tid] = since * s.rq[tid];
+                    scal[kC3 + tid] = s.c3[tid] = until * s.rk[tid];
+                }
             } else {
-                // P, and its rows' scales
+                // P, and its largest
+                float mx = 0.f;
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int i = i0 + 8 * half;
                     const double Gi = G[i];
                     const float f = s.rq[i];
-                    float p[16], mx = 0.f;
 #pragma unroll
                     for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
@@ -259,28 +288,29 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                             const int j = 8 * nt + 2 * (lane & 3) + x;
                             float v = 0.f;
                             if (j <= i) v = f * s.rk[j] * __expf((float)(Gi - G[j])) * acc[nt][2 * half + x];
-                            p[2 * nt + x] = v;
+                            p[16 * half + 2 * nt + x] = v;
                             mx = fmaxf(mx, fabsf(v));
                         }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const int e = scale_exponent(mx, 8);
-                    const float sc = pow2(e);
-                    if ((lane & 3) == 0) scal[kPS + i] = pow2(-e);
-#pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
-                        *reinterpret_cast<uint32_t*>(out + kOffP + piece_at(i, nt) + 4 * (lane & 3)) =
-                            half2_bits(p[2 * nt] * sc, p[2 * nt + 1] * sc);
                 }
-            }
-            if (tid < kC) {
-                const float since = __expf((float)G[tid]), until = __expf((float)(G[kC - 1] - G[tid]));
-                scal[kC1 + tid] = since * s.rk[tid];
-                scal[kC2 + tid] = since * s.rq[tid];
-                scal[kC3 + tid] = until * s.rk[tid];
-                if (tid == 0) scal[kEC] = __expf((float)G[kC - 1]);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                if (lane == 0) atomicMax(&s.pmax, __float_as_uint(mx));
             }
             __syncthreads();
+            if (m == 1) {
+                const int e = scale_exponent(__uint_as_float(s.pmax), 8);
+                const float sc = pow2(e);
+                if (tid == kPrepThreads - 1) {
+                    scal[kPS] = pow2(-e);
+                    scal[kEC] = __expf((float)G[kC - 1]);
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int nt = 0; nt < 8; ++nt)
+                        *reinterpret_cast<uint32_t*>(out + kOffP + piece_at(i0 + 8 * half, nt) + 4 * (lane & 3)) =
+                            half2_bits(p[16 * half + 2 * nt] * sc, p[16 * half + 2 * nt + 1] * sc);
+            }
             // inverse of (1 + A): its four 16 x 16 diagonal blocks by substitution, a thread per column
             if (tid < kC) {
                 const int o = tid & ~15, j = tid & 15;
@@ -348,20 +378,26 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                 s.T[33 + i][j] = -z[1][0]; s.T[33 + i][j + 1] = -z[1][1];
             }
             __syncthreads();
-            // T's rows with beta's columns, scaled and split: four threads a row, 16 columns each
+            // T with beta's columns, its largest value and its rows' sums: four threads a row, 16 columns each
             {
                 const int i = tid >> 2, j0 = (tid & 3) * 16;
-                float v[16], mx = 0.f;
+                float v[16], mx = 0.f, sum = 0.f;
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
                     v[x] = s.T[i][j0 + x] * beta[j0 + x];
                     mx = fmaxf(mx, fabsf(v[x]));
+                    sum += fabsf(v[x]);
                 }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const int e = scale_exponent(mx, 8);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if ((tid & 3) == 0) s.tsum[i] = sum;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                if (lane == 0) atomicMax(&s.tmax, __float_as_uint(mx));
+                __syncthreads();
+                // scaled and split
+                const int e = scale_exponent(__uint_as_float(s.tmax), 8);
                 const float sc = pow2(e);
-                if ((tid & 3) == 0) scal[kTS + i] = pow2(-e);
                 uint32_t hi[8], lo[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x) split2(v[2 * x] * sc, v[2 * x + 1] * sc, hi[x], lo[x]);
@@ -370,6 +406,28 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                     const int at = piece_at(i, (j0 >> 3) + x);
                     *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
                     *reinterpret_cast<uint4*>(out + kOffTLo + at) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
+                }
+                if (warp == 0) {
+                    float bw = 0.f, bt = 0.f, bs = 0.f;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int t = lane + 32 * x;
+                        bw = fmaxf(bw, s.c1[t] * s.ks[t]);
+                        bt = fmaxf(bt, s.tsum[t]);
+                        bs += s.c3[t] * s.tsum[t];
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        bw = fmaxf(bw, __shfl_xor_sync(0xffffffffu, bw, o));
+                        bt = fmaxf(bt, __shfl_xor_sync(0xffffffffu, bt, o));
+                        bs += __shfl_xor_sync(0xffffffffu, bs, o);
+                    }
+                    if (lane == 0) {
+                        scal[kTS] = pow2(-e);
+                        scal[kBW] = bw;
+                        scal[kBT] = bt;
+                        scal[kBS] = bs * 256.f;   // a scaled key's values are below 256
+                    }
                 }
             }
         }
@@ -381,33 +439,93 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
 // ---------------------------------------------------------------------------
 constexpr int kStageTP = kKQBytes;                        // offsets in a stage
 constexpr int kStageV = (kKQBytes + kTPBytes + 1023) / 1024 * 1024;
-constexpr int kStageBytes = kStageV + kC * kGdnDim * 2;
+// V rows, padded so that the outputs, which take their place, are written without bank conflicts
+constexpr int kVRow = kGdnDim * 2 + 16;
+constexpr int kStageBytes = (kStageV + kC * kVRow + 1023) / 1024 * 1024;
 constexpr int kStages = 3;
 constexpr int kScanBar = kStages * kStageBytes;
-constexpr int kScanMax = kScanBar + 256;                  // exponents of lane maxima: [4 exchanges][2 halves][128]
-constexpr int kScanSmem = kScanMax + 4 * 2 * 128 + 1024;
-constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr int kScanThreads = 320;
+constexpr int kScanMax = kScanBar + 256;                  // lane maxima: [state, V][2 halves][128]
+constexpr int kScanExp = kScanMax + 2 * 2 * 128 * 4;      // exponents of scales, for the output warps: [2 chunks][S0, U][128]
+constexpr int kScanSmem = kScanExp + 2 * 2 * 128 + 1024;
+// warps 0-7: state, X and U; warps 8-11: outputs; warp 12 loads, warp 13 issues the products
+constexpr int kWarpOut = 8, kWarpLoad = 12, kWarpMma = 13;
+constexpr int kScanThreads = 512;
+// registers a thread after the split, of 128 at launch: 2 x 192 + 88 + 40 = 4 x 128
+constexpr int kRegsMain = 192, kRegsOut = 88, kRegsRest = 40;
+static_assert(2 * kRegsMain + kRegsOut + kRegsRest <= 4 * 128, "the split must fit what the launch has");
 static_assert(kScanSmem <= 227 * 1024, "shared memory per CTA");
 
-// tensor memory columns: S0 as hi [0, 64) and lo [64, 128), then the state's increment [0, 128) in FP32;
-// W; X, then the scaled U, as hi and lo (32 each); Q S0; U, then P U; U as hi
-constexpr uint32_t kTmS = 0, kTmW = 128, kTmX = 192, kTmQ = 256, kTmU = 320, kTmUh = 384, kTmCols = 512;
+// tensor memory columns: S0 as hi and lo (64 each); W (64) and U (64), then over both the state's increment;
+// X, then the scaled U, as hi and lo (32 each); Q S0; P U; U as hi (32)
+constexpr uint32_t kTmS = 0, kTmW = 128, kTmU = 192, kTmD = 128, kTmX = 256, kTmQ = 320, kTmP = 384, kTmUh = 448, kTmCols = 512;
 
 enum ScanBar {
     kbFull = 0,      // [3] the stage's loads landed (tx bytes)
-    kbEmpty = 3,     // [3] 8 warps have read the stage, and every product that reads it is complete
+    kbEmpty = 3,     // [3] 12 warps are done with the stage, as is every product and store that reads it
     kbS = 6,         // 8 warps: S0 in tensor memory
     kbX = 7,         // 8 warps: X in tensor memory
     kbU = 8,         // 8 warps: U and the scaled U in tensor memory
-    kbWDone = 9,     // commits: W; Q S0; U; the state's increment; P U
-    kbQDone = 10,
+    kbO = 9,         // 4 warps: Q S0 and P U read
+    kbWDone = 10,    // commits: W; U (and Q S0 before it); the state's increment; P U
     kbUDone = 11,
     kbDDone = 12,
     kbPDone = 13,
     kbDrain = 14,    // commit after the last product, also of an abandoned CTA
     kScanBars = 15
 };
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
+
+// two FP32 operations an instruction
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ f2 pack2(uint32_t a, uint32_t b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// the FP16 pair (hi, lo) of two values
+__device__ __forceinline__ void split2(f2 v, uint32_t& hi, uint32_t& lo) {
+    const float2 x = unpack2(v);
+    hi = half2_bits(x.x, x.y);
+    float d0, d1;   // hi - x
+    asm("sub.rn.f32.f16 %0, %1, %2;\n" : "=f"(d0) : "h"((uint16_t)(hi & 0xffffu)), "f"(x.x));
+    asm("sub.rn.f32.f16 %0, %1, %2;\n" : "=f"(d1) : "h"((uint16_t)(hi >> 16)), "f"(x.y));
+    lo = half2_bits(-d0, -d1);
+}
+__device__ __forceinline__ float absmax(float m, f2 v) {
+    const float2 x = unpack2(v);
+    asm("max.abs.f32 %0, %0, %1, %2;\n" : "+f"(m) : "f"(x.x), "f"(x.y));
+    return m;
+}
+// four consecutive floats of shared memory, as two pairs
+__device__ __forceinline__ void lds4(const float* p, f2& a, f2& b) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(p);
+    a = v.x;
+    b = v.y;
+}
 
 __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_constant__ DeltaArgs a, int NC) {
     extern __shared__ uint8_t smem_raw[];
@@ -417,7 +535,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kScanBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kScanBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
-    int8_t* maxima = reinterpret_cast<int8_t*>(smem + kScanMax);
+    float* maxima = reinterpret_cast<float*>(smem + kScanMax);
+    int8_t* exps = reinterpret_cast<int8_t*>(smem + kScanExp);
     grid_dep_wait();
     grid_dep_launch();
     const int len = seq_len(a.lens, b, a.n, a.status, false);
@@ -426,9 +545,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(&bars[kbFull + i], 1);
-            ptx::mbar_init(&bars[kbEmpty + i], 8);
+            ptx::mbar_init(&bars[kbEmpty + i], 12);
         }
         for (int i = kbS; i <= kbU; ++i) ptx::mbar_init(&bars[i], 8);
+        ptx::mbar_init(&bars[kbO], 4);
         for (int i = kbWDone; i < kScanBars; ++i) ptx::mbar_init(&bars[i], 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -443,245 +563,325 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     const uint32_t tmem = *tmem_holder;
     bool ok = true;
 
-    if (warp == kWarpLoad) {
-        // ---------------- loads: a stage is the chunk's K and Q, its T, P and scalars, and its V rows ----------------
-        const uint8_t* kq = a.ws + ((int64_t)b * a.HK + kh) * NC * kKQBytes;
-        const uint8_t* tp = a.ws + (int64_t)a.B * a.HK * NC * kKQBytes + (int64_t)unit * NC * kTPBytes;
-        const uint16_t* v = a.qkv + (int64_t)b * a.n * a.C + (2 * a.HK + h) * kGdnDim;
-        int issued = 0;
-        for (int c = 0; c < nc; ++c) {
-            const int st = c % kStages;
-            if (c >= kStages && !ptx::mbar_wait_warp(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag, a.status)) break;
-            issued = c + 1;
-            uint8_t* stage = smem + st * kStageBytes;
-            const int rows = min(len - c * kC, kC);
-            if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(&bars[kbFull + st], kKQBytes + kTPBytes + rows * kGdnDim * 2);
-                ptx::bulk_load(stage, kq + (int64_t)c * kKQBytes, kKQBytes, &bars[kbFull + st]);
-                ptx::bulk_load(stage + kStageTP, tp + (int64_t)c * kTPBytes, kTPBytes, &bars[kbFull + st]);
-            }
-            __syncwarp();
-            for (int i = lane; i < rows; i += 32)
-                ptx::bulk_load(stage + kStageV + i * kGdnDim * 2, v + (int64_t)(c * kC + i) * a.C, kGdnDim * 2, &bars[kbFull + st]);
-        }
-        // what was asked for has landed before the CTA ends
-        for (int c = max(0, issued - kStages); c < issued; ++c)
-            ptx::mbar_wait_drain(&bars[kbFull + c % kStages], (c / kStages) & 1, a.status);
-    } else if (warp == kWarpMma) {
-        // ---------------- products ----------------
-        constexpr uint32_t id64 = ptx::idesc_f16_f32(128, 64, false, false);
-        constexpr uint32_t id128 = ptx::idesc_f16_f32(128, 128, false, true);
-        auto kmajor = [](uint32_t base, int ks) {   // 16 values of the rows of an image
-            return ptx::smem_desc(base + ks * 32, 16, 1024, ptx::kSwizzle128B);
-        };
-        for (int c = 0; c < nc; ++c) {
-            const int st = c % kStages;
-            const uint32_t kb = ptx::smem_u32(smem + st * kStageBytes), tb = kb + kStageTP;
-            ok = ptx::mbar_wait_warp(&bars[kbFull + st], (c / kStages) & 1, abort_flag, a.status);
-            if (!ok) break;
-            ok = ptx::mbar_wait_warp(&bars[kbS], c & 1, abort_flag, a.status);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (lane == 0) {
-                for (int ks = 0; ks < 8; ++ks)
-                    ptx::mma_ts1(tmem + kTmW, tmem + kTmS + 8 * ks, kmajor(kb + (ks >> 2) * kTile, ks & 3), id64, ks > 0);
-                for (int ks = 0; ks < 8; ++ks)
-                    ptx::mma_ts1(tmem + kTmW, tmem + kTmS + 64 + 8 * ks, kmajor(kb + (ks >> 2) * kTile, ks & 3), id64, 1);
-                ptx::mma_commit1(&bars[kbWDone]);
-                for (int ks = 0; ks < 8; ++ks)
-                    ptx::mma_ts1(tmem + kTmQ, tmem + kTmS + 8 * ks, kmajor(kb + (2 + (ks >> 2)) * kTile, ks & 3), id64, ks > 0);
-                ptx::mma_commit1(&bars[kbQDone]);
-            }
-            __syncwarp();
-            ok = ptx::mbar_wait_warp(&bars[kbX], c & 1, abort_flag, a.status);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (lane == 0) {
-                for (int ks = 0; ks < 4; ++ks) {
-                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 8 * ks, kmajor(tb, ks), id64, ks > 0);
-                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 32 + 8 * ks, kmajor(tb, ks), id64, 1);
-                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 8 * ks, kmajor(tb + kOffTLo, ks), id64, 1);
+    if (warp >= kWarpLoad) {
+        regs_down<kRegsRest>();
+        if (warp == kWarpLoad) {
+            // ---------------- loads: a stage is the chunk's K and Q, its T, P and scalars, and its V rows ----------------
+            const uint8_t* kq = a.ws + ((int64_t)b * a.HK + kh) * NC * kKQBytes;
+            const uint8_t* tp = a.ws + (int64_t)a.B * a.HK * NC * kKQBytes + (int64_t)unit * NC * kTPBytes;
+            const uint16_t* v = a.qkv + (int64_t)b * a.n * a.C + (2 * a.HK + h) * kGdnDim;
+            int issued = 0;
+            for (int c = 0; c < nc; ++c) {
+                const int st = c % kStages;
+                if (c >= kStages && !ptx::mbar_wait_warp(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag, a.status)) break;
+                issued = c + 1;
+                uint8_t* stage = smem + st * kStageBytes;
+                const int rows = min(len - c * kC, kC);
+                if (lane == 0) {
+                    ptx::mbar_arrive_expect_tx(&bars[kbFull + st], kKQBytes + kTPBytes + rows * kGdnDim * 2);
+                    ptx::bulk_load(stage, kq + (int64_t)c * kKQBytes, kKQBytes, &bars[kbFull + st]);
+                    ptx::bulk_load(stage + kStageTP, tp + (int64_t)c * kTPBytes, kTPBytes, &bars[kbFull + st]);
                 }
-                ptx::mma_commit1(&bars[kbUDone]);
+                __syncwarp();
+                for (int i = lane; i < rows; i += 32)
+                    ptx::bulk_load(stage + kStageV + i * kVRow, v + (int64_t)(c * kC + i) * a.C, kGdnDim * 2, &bars[kbFull + st]);
             }
-            __syncwarp();
-            ok = ptx::mbar_wait_warp(&bars[kbU], c & 1, abort_flag, a.status);
-            if (!ok) break;
-            ptx::tc_fence_after();
-            if (lane == 0) {
-                for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t kd = ptx::smem_desc(kb + ks * 16 * 128, kTile, 1024, ptx::kSwizzle128B);
-                    ptx::mma_ts1(tmem + kTmS, tmem + kTmX + 8 * ks, kd, id128, ks > 0);
-                    ptx::mma_ts1(tmem + kTmS, tmem + kTmX + 32 + 8 * ks, kd, id128, 1);
+            // what was asked for has landed before the CTA ends
+            for (int c = max(0, issued - kStages); c < issued; ++c)
+                ptx::mbar_wait_drain(&bars[kbFull + c % kStages], (c / kStages) & 1, a.status);
+        } else if (warp == kWarpMma) {
+            // ---------------- products ----------------
+            // The warp computes the operands together and one elected lane issues: a branch taken by one
+            // lane instead costs about 100 cycles an instruction, three times what its product takes.
+            constexpr uint32_t id64 = ptx::idesc_f16_f32(128, 64, false, false);
+            constexpr uint32_t id128 = ptx::idesc_f16_f32(128, 128, false, true);
+            const uint32_t go = ptx::elect_one();
+            // 16 values of the rows of an image are 32 bytes: 2 in the descriptor's address field
+            for (int c = 0; c < nc; ++c) {
+                const int st = c % kStages;
+                const uint32_t kb = ptx::smem_u32(smem + st * kStageBytes), tb = kb + kStageTP;
+                const uint64_t dk = ptx::smem_desc(kb, 16, 1024, ptx::kSwizzle128B);
+                const uint64_t dt = ptx::smem_desc(tb, 16, 1024, ptx::kSwizzle128B);
+                const uint64_t dd = ptx::smem_desc(kb, kTile, 1024, ptx::kSwizzle128B);
+                constexpr uint64_t kImage = kTile >> 4;
+                ok = ptx::mbar_wait_warp(&bars[kbFull + st], (c / kStages) & 1, abort_flag, a.status);
+                if (!ok) break;
+                ok = ptx::mbar_wait_warp(&bars[kbS], c & 1, abort_flag, a.status);
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 16; ++ks)   // hi, then lo
+                    ptx::mma_ts1(tmem + kTmW, tmem + kTmS + 8 * ks, dk + ((ks >> 2) & 1) * kImage + 2 * (ks & 3), id64, ks > 0, go);
+                ptx::mma_commit1(&bars[kbWDone], go);
+                if (c > 0) {
+                    ok = ptx::mbar_wait_warp(&bars[kbO], (c - 1) & 1, abort_flag, a.status);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
                 }
-                ptx::mma_commit1(&bars[kbDDone]);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    ptx::mma_ts1(tmem + kTmQ, tmem + kTmS + 8 * ks, dk + (2 + (ks >> 2)) * kImage + 2 * (ks & 3), id64, ks > 0, go);
+                ok = ptx::mbar_wait_warp(&bars[kbX], c & 1, abort_flag, a.status);
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 8 * ks, dt + 2 * ks, id64, ks > 0, go);
+                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 32 + 8 * ks, dt + 2 * ks, id64, 1, go);
+                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 8 * ks, dt + (kOffTLo >> 4) + 2 * ks, id64, 1, go);
+                }
+                ptx::mma_commit1(&bars[kbUDone], go);
+                ok = ptx::mbar_wait_warp(&bars[kbU], c & 1, abort_flag, a.status);
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {   // 16 rows are 2 KiB
+                    ptx::mma_ts1(tmem + kTmD, tmem + kTmX + 8 * ks, dd + 128 * ks, id128, ks > 0, go);
+                    ptx::mma_ts1(tmem + kTmD, tmem + kTmX + 32 + 8 * ks, dd + 128 * ks, id128, 1, go);
+                }
+                ptx::mma_commit1(&bars[kbDDone], go);
+#pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    ptx::mma_ts1(tmem + kTmU, tmem + kTmUh + 8 * ks, kmajor(tb + kOffP, ks), id64, ks > 0);
-                ptx::mma_commit1(&bars[kbPDone]);
+                    ptx::mma_ts1(tmem + kTmP, tmem + kTmUh + 8 * ks, dt + (kOffP >> 4) + 2 * ks, id64, ks > 0, go);
+                ptx::mma_commit1(&bars[kbPDone], go);
+            }
+            ptx::mma_commit1(&bars[kbDrain], go);
+            __syncwarp();
+            ptx::mbar_wait_drain(&bars[kbDrain], 0, a.status);
+        }
+    } else if (warp >= kWarpOut) {
+        regs_down<kRegsOut>();
+        // ---------------- outputs: a warp's 32 lanes (value columns), read as fragments of 16 x 8 ----------------
+        const int w = warp & 3, col0 = 32 * w;
+        const uint32_t tl = tmem + ((uint32_t)col0 << 16);
+        const int64_t step = (int64_t)a.HV * kGdnDim;
+        uint16_t* out = a.out + (int64_t)b * a.n * step + h * kGdnDim;
+        // stmatrix: this lane's row (a token, within two groups of 8) and 8 columns
+        const int st_off = ((lane & 7) + ((lane >> 4) << 3)) * kVRow + (col0 + ((lane >> 3) & 1) * 8) * 2;
+        for (int c = 0; c < nc; ++c, out += kC * step) {
+            const int st = c % kStages;
+            uint8_t* stage = smem + st * kStageBytes;
+            const float* scal = reinterpret_cast<const float*>(stage + kStageTP + kOffScal);
+            const int left = len - c * kC;
+            ok = ptx::mbar_wait_warp(&bars[kbFull + st], (c / kStages) & 1, abort_flag, a.status) && ok;
+            ok = ptx::mbar_wait_warp(&bars[kbU], c & 1, abort_flag, a.status) && ok;   // the scales
+            const float inv_p = scal[kPS];
+            ok = ptx::mbar_wait_warp(&bars[kbPDone], c & 1, abort_flag, a.status) && ok;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int hl = 0; hl < 2; ++hl) {            // 16 columns
+                f2 is[2], iu[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int8_t* e = exps + (c & 1) * 256 + col0 + 16 * hl + 8 * r + (lane >> 2);
+                    const float fs = pow2(-(int)e[0]), fu = pow2(-(int)e[128]) * inv_p;
+                    is[r] = pack2(fs, fs);
+                    iu[r] = pack2(fu, fu);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {           // 32 tokens
+                    uint32_t q[16], y[16], o[8];
+                    ptx::tmem_ld_frag4(tl + ((uint32_t)(16 * hl) << 16) + kTmQ + 32 * p, q);
+                    ptx::tmem_ld_frag4(tl + ((uint32_t)(16 * hl) << 16) + kTmP + 32 * p, y);
+                    ptx::tmem_wait_ld();
+                    if (hl == 1 && p == 1) {            // Q S0 and P U are read
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(&bars[kbO]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const f2 c2 = *reinterpret_cast<const f2*>(scal + kC2 + 32 * p + 8 * j + 2 * (lane & 3));
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const f2 x = mul2(pack2(q[4 * j + 2 * r], q[4 * j + 2 * r + 1]), mul2(c2, is[r]));
+                            const float2 v = unpack2(fma2(pack2(y[4 * j + 2 * r], y[4 * j + 2 * r + 1]), iu[r], x));
+                            o[2 * j + r] = pack_bf16(v.x, v.y);
+                        }
+                    }
+                    const uint32_t to = ptx::smem_u32(stage + kStageV) + st_off + 32 * p * kVRow + 32 * hl;
+                    stsm4_trans(to, o[0], o[1], o[2], o[3]);
+                    stsm4_trans(to + 16 * kVRow, o[4], o[5], o[6], o[7]);
+                }
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::named_bar_sync(5, 128);
+            const int t = 16 * w + lane;                // a row (256 bytes) a lane
+            if (lane < 16 && t < left) {
+                bulk_store(out + t * step, stage + kStageV + t * kVRow, kGdnDim * 2);
+                ptx::bulk_commit();
+                ptx::bulk_wait_read_all();
             }
             __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);
         }
-        if (lane == 0) ptx::mma_commit1(&bars[kbDrain]);
-        __syncwarp();
-        ptx::mbar_wait_drain(&bars[kbDrain], 0, a.status);
     } else {
+        regs_up<kRegsMain>();
         // ---------------- a thread: lane (value column) `row`, half `wg` of the keys or tokens ----------------
         const int wg = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const int pair_bar = 1 + (warp & 3);
-        // the scale of this lane's values, whose largest in this half is m, from both halves' exponents:
-        // offered, exchanged (which also orders the two warps' tensor-memory accesses), taken
-        auto offer = [&](int which, float m) {
-            maxima[(2 * which + wg) * 128 + row] = (int8_t)min(max(exponent_of(m), -110), 127);
-        };
-        auto exchange = [&]() {
-            ptx::tc_fence_before();
-            ptx::named_bar_sync(pair_bar, 64);
-            ptx::tc_fence_after();
-        };
-        auto take = [&](int which) {
-            return scale_of_exponent(max(maxima[2 * which * 128 + row], maxima[(2 * which + 1) * 128 + row]), 15);
-        };
         auto signal = [&](int bar) {
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars[bar]);
         };
-        float S[64];
+        // the larger of the two halves' values, of this lane's state and V
+        auto exchange = [&](float& ms, float& mv) {
+            maxima[wg * 128 + row] = ms;
+            maxima[(2 + wg) * 128 + row] = mv;
+            ptx::named_bar_sync(pair_bar, 64);
+            ms = fmaxf(ms, maxima[(wg ^ 1) * 128 + row]);
+            mv = fmaxf(mv, maxima[(2 + (wg ^ 1)) * 128 + row]);
+        };
+        // The lane's scales are powers of two from bounds on its values, all known before the products they
+        // are for: of the state at the start (its own maximum), of X (V and the keys' sums), of U and the
+        // state at the end (X and T's sums).  A bound may be some binades loose: the pairs reach 2^-39 of it.
+        f2 S[32];   // times 2^es: keys 64 wg + 2 i, 2 i + 1
+        int es;
         float* gs = a.state + ((int64_t)unit * kGdnDim + 64 * wg) * kGdnDim + row;
+        {
 #pragma unroll
-        for (int i = 0; i < 64; ++i) S[i] = gs[i * kGdnDim];
-        float inv_s = 1.f;
-        auto put_state = [&]() {
-            float m[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int i = 0; i < 32; ++i) S[i] = pack2(gs[2 * i * kGdnDim], gs[(2 * i + 1) * kGdnDim]);
+            float ms = 0.f, none = 0.f;
 #pragma unroll
-            for (int i = 0; i < 64; ++i) m[i & 3] = fmaxf(m[i & 3], fabsf(S[i]));
-            offer(0, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-            exchange();
-            const int e = take(0);
-            const float f = pow2(e);
-            inv_s = pow2(-e);
+            for (int i = 0; i < 32; ++i) ms = absmax(ms, S[i]);
+            exchange(ms, none);
+            ptx::named_bar_sync(pair_bar, 64);   // both have read, before the first chunk's exchange
+            es = scale_exponent(ms, 15);
+            const f2 f = pack2(pow2(es), pow2(es));
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[i] = mul2(S[i], f);
+        }
+        auto put_state = [&](int c) {
+            if (wg == 0) exps[(c & 1) * 256 + row] = (int8_t)es;
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) split2(S[32 * p + 2 * i] * f, S[32 * p + 2 * i + 1] * f, hi[i], lo[i]);
+                for (int i = 0; i < 16; ++i) split2(S[16 * p + i], hi[i], lo[i]);
                 ptx::tmem_st16(tl + kTmS + 32 * wg + 16 * p, hi);
                 ptx::tmem_st16(tl + kTmS + 64 + 32 * wg + 16 * p, lo);
             }
             signal(kbS);
         };
-        put_state();
+        constexpr float kCap = 1.2676506e30f;   // 2^100: a factor beyond it multiplies a zero, and must not be infinite
+        put_state(0);
         for (int c = 0; c < nc; ++c) {
             const int st = c % kStages;
             const uint8_t* stage = smem + st * kStageBytes;
-            const float* scal = reinterpret_cast<const float*>(stage + kStageTP + kOffScal);
-            const uint16_t* vs = reinterpret_cast<const uint16_t*>(stage + kStageV) + 32 * wg * kGdnDim + row;
+            const float* one = reinterpret_cast<const float*>(stage + kStageTP + kOffScal);
+            const float* scal = one + 32 * wg;   // this half's tokens
+            const uint16_t* vs = reinterpret_cast<const uint16_t*>(stage + kStageV + 32 * wg * kVRow) + row;
             const int left = len - c * kC - 32 * wg;   // tokens of this half
             // (an abandoned CTA goes on through its barriers, on values that nobody uses)
             ok = ptx::mbar_wait_warp(&bars[kbFull + st], (c / kStages) & 1, abort_flag, a.status) && ok;
+            // while W is computed: V, the bounds and the scales
             uint32_t x[32];
-            float v[32];
+            f2 v[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = bf16_float(vs[i * kGdnDim]);
+            for (int i = 0; i < 16; ++i) v[i] = pack2(bf16_float(vs[i * kVRow]), bf16_float(vs[i * kVRow + kVRow / 2]));
+            if (left < 32) {   // tokens past the end: whatever the stage held there (their K is 0, so their X will be)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 d = unpack2(v[i]);
+                    v[i] = pack2(2 * i < left ? d.x : 0.f, 2 * i + 1 < left ? d.y : 0.f);
+                }
+            }
+            float ms[2] = {0.f, 0.f}, mv[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ms[i & 1] = absmax(ms[i & 1], S[i]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mv[i & 1] = absmax(mv[i & 1], v[i]);
+            float smax = fmaxf(ms[0], ms[1]), vmax = fmaxf(mv[0], mv[1]);
+            exchange(smax, vmax);
+            const float inv_s = pow2(-es);
+            smax *= inv_s;
+            const float keep = one[kEC], bx = fmaf(one[kBW], smax, vmax);
+            const int ex = scale_exponent(bx, 15), eu = scale_exponent(one[kBT] * bx, 15);
+            const int es1 = scale_exponent(fmaf(one[kBS], bx, keep * smax), 15);
+            const float fx = pow2(ex), from_x = pow2(-ex) * one[kTS];
+            const float cw = -fminf(inv_s * fx, kCap);                // W to X's scale
+            const float cu = fminf(pow2(eu) * from_x, kCap);          // U's accumulator to U's scale
+            const float cd = fminf(pow2(es1) * from_x, kCap);         // and, with c3, to the new state's
+            const float ck = fminf(keep * inv_s * pow2(es1), kCap);   // the state to its new scale
+            {
+                const f2 f = pack2(fx, fx);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], f);
+            }
+            // X
             ok = ptx::mbar_wait_warp(&bars[kbWDone], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmW + 32 * wg, x);
             ptx::tmem_wait_ld();
-            float inv_x;
             {
-                float m[2] = {0.f, 0.f};
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float w = __uint_as_float(x[i]) * inv_s;
-                    const float d = i < left ? fmaf(-scal[kC1 + 32 * wg + i], w, v[i]) : 0.f;
-                    v[i] = d;
-                    m[i & 1] = fmaxf(m[i & 1], fabsf(d));
-                }
-                offer(1, fmaxf(m[0], m[1]));
-                exchange();
-                const int e = take(1);
-                const float f = pow2(e);
-                inv_x = pow2(-e);
+                const f2 cw2 = pack2(cw, cw);
                 uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) split2(v[2 * i] * f, v[2 * i + 1] * f, hi[i], lo[i]);
+                for (int i = 0; i < 16; i += 2) {
+                    f2 c1[2];
+                    lds4(scal + kC1 + 2 * i, c1[0], c1[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        split2(fma2(pack2(x[2 * (i + j)], x[2 * (i + j) + 1]), mul2(c1[j], cw2), v[i + j]), hi[i + j], lo[i + j]);
+                }
                 ptx::tmem_st16(tl + kTmX + 16 * wg, hi);
                 ptx::tmem_st16(tl + kTmX + 32 + 16 * wg, lo);
                 signal(kbX);
             }
-            // Q S0 while U is computed
-            float o[32];
-            ok = ptx::mbar_wait_warp(&bars[kbQDone], c & 1, abort_flag, a.status) && ok;
-            ptx::tc_fence_after();
-            ptx::tmem_ld32(tl + kTmQ + 32 * wg, x);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(x[i]) * inv_s * scal[kC2 + 32 * wg + i];
             // U, and U scaled for the state
+            if (wg == 0) exps[(c & 1) * 256 + 128 + row] = (int8_t)eu;
             ok = ptx::mbar_wait_warp(&bars[kbUDone], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmU + 32 * wg, x);
             ptx::tmem_wait_ld();
-            float inv_u, inv_d;
             {
-                float mu = 0.f, md = 0.f;
+                const f2 cu2 = pack2(cu, cu), cd2 = pack2(cd, cd);
+                uint32_t hi[16], lo[16], u[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float u = __uint_as_float(x[i]) * inv_x * scal[kTS + 32 * wg + i];
-                    x[i] = __float_as_uint(u);
-                    v[i] = u * scal[kC3 + 32 * wg + i];
-                    mu = fmaxf(mu, fabsf(u));
-                    md = fmaxf(md, fabsf(v[i]));
+                for (int i = 0; i < 16; i += 2) {
+                    f2 c3[2];
+                    lds4(scal + kC3 + 2 * i, c3[0], c3[1]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f2 y = pack2(x[2 * (i + j)], x[2 * (i + j) + 1]);
+                        const float2 w = unpack2(mul2(y, cu2));
+                        u[i + j] = half2_bits(w.x, w.y);
+                        split2(mul2(y, mul2(c3[j], cd2)), hi[i + j], lo[i + j]);
+                    }
                 }
-                offer(2, md);
-                offer(3, mu);
-                exchange();
-                const int ed = take(2), eu = take(3);
-                const float fd = pow2(ed), fu = pow2(eu);
-                inv_d = pow2(-ed);
-                inv_u = pow2(-eu);
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) split2(v[2 * i] * fd, v[2 * i + 1] * fd, hi[i], lo[i]);
                 ptx::tmem_st16(tl + kTmX + 16 * wg, hi);
                 ptx::tmem_st16(tl + kTmX + 32 + 16 * wg, lo);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    hi[i] = half2_bits(__uint_as_float(x[2 * i]) * fu, __uint_as_float(x[2 * i + 1]) * fu);
-                ptx::tmem_st16(tl + kTmUh + 16 * wg, hi);
+                ptx::tmem_st16(tl + kTmUh + 16 * wg, u);
                 signal(kbU);
             }
+            if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);   // (the output warps wait for the products)
             // the state
-            const float keep = scal[kEC];
             ok = ptx::mbar_wait_warp(&bars[kbDDone], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
+            es = es1;
+            {
+                const f2 k2 = pack2(ck, ck);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                ptx::tmem_ld32(tl + kTmS + 64 * wg + 32 * p, x);
-                ptx::tmem_wait_ld();
+                for (int p = 0; p < 2; ++p) {
+                    ptx::tmem_ld32(tl + kTmD + 64 * wg + 32 * p, x);
+                    ptx::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) S[32 * p + i] = fmaf(S[32 * p + i], keep, __uint_as_float(x[i]) * inv_d);
+                    for (int i = 0; i < 16; ++i) S[16 * p + i] = fma2(S[16 * p + i], k2, pack2(x[2 * i], x[2 * i + 1]));
+                }
             }
-            if (c + 1 < nc) put_state();
-            // the outputs
-            ok = ptx::mbar_wait_warp(&bars[kbPDone], c & 1, abort_flag, a.status) && ok;
-            ptx::tc_fence_after();
-            ptx::tmem_ld32(tl + kTmU + 32 * wg, x);
-            ptx::tmem_wait_ld();
-            uint16_t* out = a.out + (((int64_t)b * a.n + c * kC + 32 * wg) * a.HV + h) * kGdnDim + row;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float y = fmaf(__uint_as_float(x[i]) * inv_u, scal[kPS + 32 * wg + i], o[i]);
-                if (i < left) out[(int64_t)i * a.HV * kGdnDim] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-            }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);
+            if (c + 1 < nc) put_state(c + 1);
         }
         if (ok) {
+            const float f = pow2(-es);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) gs[i * kGdnDim] = S[i];
+            for (int i = 0; i < 32; ++i) {
+                const float2 x = unpack2(S[i]);
+                gs[2 * i * kGdnDim] = x.x * f;
+                gs[(2 * i + 1) * kGdnDim] = x.y * f;
+            }
         }
     }
     ptx::tc_fence_before();
