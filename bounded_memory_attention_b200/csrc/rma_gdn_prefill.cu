@@ -31,6 +31,8 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "rma_gdn.cuh"
 #include "sm100_ptx.cuh"
 
@@ -87,10 +89,11 @@ __device__ __forceinline__ void stsm4_trans(uint32_t addr, uint32_t r0, uint32_t
                  "r"(r2), "r"(r3)
                  : "memory");
 }
-// Copy `bytes` (a multiple of 16) of shared memory to global memory, both 16-byte aligned.
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n" ::"l"(reinterpret_cast<uint64_t>(dst)),
-                 "r"(ptx::smem_u32(src)), "r"(bytes)
+// TMA store of one box from shared memory (bulk-group completion).
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(ptx::smem_u32(src))
                  : "memory");
 }
 
@@ -438,40 +441,52 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
 // launch 2
 // ---------------------------------------------------------------------------
 constexpr int kStageTP = kKQBytes;                        // offsets in a stage
-constexpr int kStageV = (kKQBytes + kTPBytes + 1023) / 1024 * 1024;
-// V rows, padded so that the outputs, which take their place, are written without bank conflicts
-constexpr int kVRow = kGdnDim * 2 + 16;
-constexpr int kStageBytes = (kStageV + kC * kVRow + 1023) / 1024 * 1024;
+constexpr int kStageV = (kKQBytes + kTPBytes + 1023) / 1024 * 1024;   // V rows; then, in their place, the outputs
+constexpr int kStageBytes = kStageV + kC * kGdnDim * 2;
 constexpr int kStages = 3;
 constexpr int kScanBar = kStages * kStageBytes;
 constexpr int kScanMax = kScanBar + 256;                  // lane maxima: [state, V][2 halves][128]
 constexpr int kScanExp = kScanMax + 2 * 2 * 128 * 4;      // exponents of scales, for the output warps: [2 chunks][S0, U][128]
 constexpr int kScanSmem = kScanExp + 2 * 2 * 128 + 1024;
-// warps 0-7: state, X and U; warps 8-11: outputs; warp 12 loads, warp 13 issues the products
+// warps 0-3 and 4-7: state, X and U, by halves; warps 8-11: outputs; warp 12 loads, warp 13 issues the products
 constexpr int kWarpOut = 8, kWarpLoad = 12, kWarpMma = 13;
 constexpr int kScanThreads = 512;
 // registers a thread after the split, of 128 at launch: 2 x 192 + 88 + 40 = 4 x 128
 constexpr int kRegsMain = 192, kRegsOut = 88, kRegsRest = 40;
 static_assert(2 * kRegsMain + kRegsOut + kRegsRest <= 4 * 128, "the split must fit what the launch has");
+static_assert(kStages == 3, "the issuing warp goes through the stages by name");
 static_assert(kScanSmem <= 227 * 1024, "shared memory per CTA");
 
-// tensor memory columns: S0 as hi and lo (64 each); W (64) and U (64), then over both the state's increment;
-// X, then the scaled U, as hi and lo (32 each); Q S0; P U; U as hi (32)
-constexpr uint32_t kTmS = 0, kTmW = 128, kTmU = 192, kTmD = 128, kTmX = 256, kTmQ = 320, kTmP = 384, kTmUh = 448, kTmCols = 512;
+// Tensor memory columns; a half is 64 keys of the state, or 32 tokens of the rest.  A thread overwrites
+// only columns that it has read itself, and only after the products that read them are complete.
+//   S   [0, 128)    per half: S0 as hi, lo (32 + 32); then the state's increment (64, FP32)
+//   W   [128, 192)  per half: W (32); then the scaled U as hi, lo (16 + 16)
+//   X   [192, 256)  per half: X as hi, lo (16 + 16)
+//   U   [256, 320)  per half: U (32); then U as hi (16)
+//   Q S0 [320, 384),  P U [384, 448)
+constexpr uint32_t kTmS = 0, kTmW = 128, kTmX = 192, kTmU = 256, kTmQ = 320, kTmP = 384, kTmCols = 512;
+
+// named barriers: a half's lane maxima offered by a warp to the other half's (8), the output warps
+constexpr int kBarPair = 1, kBarOut = 9;
 
 enum ScanBar {
     kbFull = 0,      // [3] the stage's loads landed (tx bytes)
-    kbEmpty = 3,     // [3] 12 warps are done with the stage, as is every product and store that reads it
-    kbS = 6,         // 8 warps: S0 in tensor memory
-    kbX = 7,         // 8 warps: X in tensor memory
-    kbU = 8,         // 8 warps: U and the scaled U in tensor memory
-    kbO = 9,         // 4 warps: Q S0 and P U read
-    kbWDone = 10,    // commits: W; U (and Q S0 before it); the state's increment; P U
-    kbUDone = 11,
-    kbDDone = 12,
-    kbPDone = 13,
-    kbDrain = 14,    // commit after the last product, also of an abandoned CTA
-    kScanBars = 15
+    kbEmpty = 3,     // [3] 8 warps and the stores are done with the stage (and every product that reads it)
+    kbS = 6,         // [2] 4 warps: their half of S0 in tensor memory
+    kbX = 8,         // [2] 4 warps: X
+    kbU = 10,        // [2] 4 warps: U and the scaled U
+    kbO = 12,        // 4 warps: Q S0 and P U read
+    kbWDone = 13,    // [2] commits: W of a half's tokens
+    kbUDone = 15,    // [2] U of a half's tokens (and all before, Q S0 among it)
+    kbDDone = 17,    // [2] the state's increment, a half of the keys
+    kbPDone = 19,    // P U, and with it every product of the chunk
+    kbDrain = 20,    // commit after the last product, also of an abandoned CTA
+    kScanBars = 21
+};
+
+struct ScanMaps {
+    CUtensorMap v;     // qkv as [batch n][C]: boxes of 128 columns x 64 rows, linear
+    CUtensorMap out;   // out as [batch n][HV 128]: boxes of 64 columns x 64 rows, 128-byte swizzle
 };
 
 template <int N>
@@ -527,9 +542,12 @@ __device__ __forceinline__ void lds4(const float* p, f2& a, f2& b) {
     b = v.y;
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_constant__ DeltaArgs a, int NC) {
+__global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_constant__ DeltaArgs a,
+                                                                   const __grid_constant__ ScanMaps maps, int NC) {
     extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // the same place as a shared-memory address and as a pointer
+    const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int unit = blockIdx.x, b = unit / a.HV, h = unit % a.HV, kh = h / (a.HV / a.HK);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kScanBar);
@@ -545,10 +563,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             ptx::mbar_init(&bars[kbFull + i], 1);
-            ptx::mbar_init(&bars[kbEmpty + i], 12);
+            ptx::mbar_init(&bars[kbEmpty + i], 9);
         }
-        for (int i = kbS; i <= kbU; ++i) ptx::mbar_init(&bars[i], 8);
-        ptx::mbar_init(&bars[kbO], 4);
+        for (int i = kbS; i <= kbO; ++i) ptx::mbar_init(&bars[i], 4);
         for (int i = kbWDone; i < kScanBars; ++i) ptx::mbar_init(&bars[i], 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -560,7 +577,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    // all of tensor memory is this CTA's, so its first column is 0: the products' operands are then constants
+    constexpr uint32_t tmem = 0;
     bool ok = true;
 
     if (warp >= kWarpLoad) {
@@ -569,22 +587,20 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             // ---------------- loads: a stage is the chunk's K and Q, its T, P and scalars, and its V rows ----------------
             const uint8_t* kq = a.ws + ((int64_t)b * a.HK + kh) * NC * kKQBytes;
             const uint8_t* tp = a.ws + (int64_t)a.B * a.HK * NC * kKQBytes + (int64_t)unit * NC * kTPBytes;
-            const uint16_t* v = a.qkv + (int64_t)b * a.n * a.C + (2 * a.HK + h) * kGdnDim;
             int issued = 0;
             for (int c = 0; c < nc; ++c) {
                 const int st = c % kStages;
                 if (c >= kStages && !ptx::mbar_wait_warp(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag, a.status)) break;
                 issued = c + 1;
                 uint8_t* stage = smem + st * kStageBytes;
-                const int rows = min(len - c * kC, kC);
                 if (lane == 0) {
-                    ptx::mbar_arrive_expect_tx(&bars[kbFull + st], kKQBytes + kTPBytes + rows * kGdnDim * 2);
+                    ptx::mbar_arrive_expect_tx(&bars[kbFull + st], kKQBytes + kTPBytes + kC * kGdnDim * 2);
                     ptx::bulk_load(stage, kq + (int64_t)c * kKQBytes, kKQBytes, &bars[kbFull + st]);
                     ptx::bulk_load(stage + kStageTP, tp + (int64_t)c * kTPBytes, kTPBytes, &bars[kbFull + st]);
+                    // 64 rows, also past the sequence's end (not used) or the tensor's (zeros)
+                    ptx::tma_load_2d(stage + kStageV, &maps.v, &bars[kbFull + st], (2 * a.HK + h) * kGdnDim, b * a.n + c * kC);
                 }
                 __syncwarp();
-                for (int i = lane; i < rows; i += 32)
-                    ptx::bulk_load(stage + kStageV + i * kVRow, v + (int64_t)(c * kC + i) * a.C, kGdnDim * 2, &bars[kbFull + st]);
             }
             // what was asked for has landed before the CTA ends
             for (int c = max(0, issued - kStages); c < issued; ++c)
@@ -593,57 +609,95 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             // ---------------- products ----------------
             // The warp computes the operands together and one elected lane issues: a branch taken by one
             // lane instead costs about 100 cycles an instruction, three times what its product takes.
+            // T and P are lower triangular: the first half's tokens take the first half's rows and columns only.
+            constexpr uint32_t id32 = ptx::idesc_f16_f32(128, 32, false, false);
             constexpr uint32_t id64 = ptx::idesc_f16_f32(128, 64, false, false);
-            constexpr uint32_t id128 = ptx::idesc_f16_f32(128, 128, false, true);
+            constexpr uint32_t id64t = ptx::idesc_f16_f32(128, 64, false, true);
+            constexpr uint32_t id128t = ptx::idesc_f16_f32(128, 128, false, true);
+            constexpr uint32_t kImage = kTile >> 4, kHalfRows = (32 * 128) >> 4, kTLo = kOffTLo >> 4, kP = kOffP >> 4;
             const uint32_t go = ptx::elect_one();
-            // 16 values of the rows of an image are 32 bytes: 2 in the descriptor's address field
-            for (int c = 0; c < nc; ++c) {
-                const int st = c % kStages;
-                const uint32_t kb = ptx::smem_u32(smem + st * kStageBytes), tb = kb + kStageTP;
-                const uint64_t dk = ptx::smem_desc(kb, 16, 1024, ptx::kSwizzle128B);
-                const uint64_t dt = ptx::smem_desc(tb, 16, 1024, ptx::kSwizzle128B);
-                const uint64_t dd = ptx::smem_desc(kb, kTile, 1024, ptx::kSwizzle128B);
-                constexpr uint64_t kImage = kTile >> 4;
-                ok = ptx::mbar_wait_warp(&bars[kbFull + st], (c / kStages) & 1, abort_flag, a.status);
-                if (!ok) break;
-                ok = ptx::mbar_wait_warp(&bars[kbS], c & 1, abort_flag, a.status);
-                if (!ok) break;
-                ptx::tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < 16; ++ks)   // hi, then lo
-                    ptx::mma_ts1(tmem + kTmW, tmem + kTmS + 8 * ks, dk + ((ks >> 2) & 1) * kImage + 2 * (ks & 3), id64, ks > 0, go);
-                ptx::mma_commit1(&bars[kbWDone], go);
-                if (c > 0) {
-                    ok = ptx::mbar_wait_warp(&bars[kbO], (c - 1) & 1, abort_flag, a.status);
-                    if (!ok) break;
+            // One chunk, in a stage that is a constant: with it the operands are constants or uniform, and the
+            // warp spends few instructions on each product.  False when the CTA is abandoned.
+            auto chunk = [&](auto stage_c, int c) -> bool {
+                constexpr int st = decltype(stage_c)::value;
+                const uint32_t kb = smem_base + st * kStageBytes, tb = kb + kStageTP;
+                // low words of the descriptors: address and leading offset (the state's increment takes K by
+                // columns).  16 values of the rows of an image are 32 bytes: 2 in the address field
+                const uint32_t dk = (kb >> 4) | (1u << 16), dt = (tb >> 4) | (1u << 16), dd = (kb >> 4) | ((uint32_t)(kTile >> 4) << 16);
+                auto wait = [&](int bar, int phase) {
+                    const bool there = ptx::mbar_wait_warp(&bars[bar], phase & 1, abort_flag, a.status);
                     ptx::tc_fence_after();
+                    return there;
+                };
+                if (!wait(kbFull + st, c / kStages)) return false;
+                // the chunk before is complete: the scaled U lies where W goes
+                if (c > 0 && !wait(kbPDone, c - 1)) return false;
+                // W, as the halves of the state arrive; the first half's tokens are done first
+                if (!wait(kbS, c)) return false;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)   // hi, then lo
+                    ptx::mma_ts1(kTmW, kTmS + 8 * ks, dk + 2 * (ks & 3), id64, ks > 0, go);
+                if (!wait(kbS + 1, c)) return false;
+#pragma unroll
+                for (int ht = 0; ht < 2; ++ht) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        ptx::mma_ts1(kTmW + 32 * ht, kTmS + 64 + 8 * ks, dk + kImage + ht * kHalfRows + 2 * (ks & 3), id32, 1, go);
+                    ptx::mma_commit1(&bars[kbWDone + ht], go);
                 }
+                if (c > 0 && !wait(kbO, c - 1)) return false;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    ptx::mma_ts1(tmem + kTmQ, tmem + kTmS + 8 * ks, dk + (2 + (ks >> 2)) * kImage + 2 * (ks & 3), id64, ks > 0, go);
-                ok = ptx::mbar_wait_warp(&bars[kbX], c & 1, abort_flag, a.status);
-                if (!ok) break;
-                ptx::tc_fence_after();
+                    ptx::mma_ts1(kTmQ, kTmS + 64 * (ks >> 2) + 8 * (ks & 3), dk + (2 + (ks >> 2)) * kImage + 2 * (ks & 3), id64, ks > 0, go);
+                // U: the first half's X for all tokens, which is all of the first half's U; then the second half's
+                if (!wait(kbX, c)) return false;
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 8 * ks, dt + 2 * ks, id64, ks > 0, go);
-                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 32 + 8 * ks, dt + 2 * ks, id64, 1, go);
-                    ptx::mma_ts1(tmem + kTmU, tmem + kTmX + 8 * ks, dt + (kOffTLo >> 4) + 2 * ks, id64, 1, go);
+                for (int ks = 0; ks < 2; ++ks) {
+                    ptx::mma_ts1(kTmU, kTmX + 8 * ks, dt + 2 * ks, id64, ks > 0, go);
+                    ptx::mma_ts1(kTmU, kTmX + 16 + 8 * ks, dt + 2 * ks, id64, 1, go);
+                    ptx::mma_ts1(kTmU, kTmX + 8 * ks, dt + kTLo + 2 * ks, id64, 1, go);
                 }
                 ptx::mma_commit1(&bars[kbUDone], go);
-                ok = ptx::mbar_wait_warp(&bars[kbU], c & 1, abort_flag, a.status);
-                if (!ok) break;
-                ptx::tc_fence_after();
+                if (!wait(kbX + 1, c)) return false;
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {   // 16 rows are 2 KiB
-                    ptx::mma_ts1(tmem + kTmD, tmem + kTmX + 8 * ks, dd + 128 * ks, id128, ks > 0, go);
-                    ptx::mma_ts1(tmem + kTmD, tmem + kTmX + 32 + 8 * ks, dd + 128 * ks, id128, 1, go);
+                for (int ks = 0; ks < 2; ++ks) {
+                    const uint32_t t = dt + kHalfRows + 4 + 2 * ks;
+                    ptx::mma_ts1(kTmU + 32, kTmX + 32 + 8 * ks, t, id32, 1, go);
+                    ptx::mma_ts1(kTmU + 32, kTmX + 48 + 8 * ks, t, id32, 1, go);
+                    ptx::mma_ts1(kTmU + 32, kTmX + 32 + 8 * ks, t + kTLo, id32, 1, go);
                 }
-                ptx::mma_commit1(&bars[kbDDone], go);
+                ptx::mma_commit1(&bars[kbUDone + 1], go);
+                // the state's increment: the first half's tokens for all keys, then the second's for each half of them
+                if (!wait(kbU, c)) return false;
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                    ptx::mma_ts1(tmem + kTmP, tmem + kTmUh + 8 * ks, dt + (kOffP >> 4) + 2 * ks, id64, ks > 0, go);
+                for (int ks = 0; ks < 2; ++ks) {   // 16 rows are 2 KiB
+                    ptx::mma_ts1(kTmS, kTmW + 8 * ks, dd + 128 * ks, id128t, ks > 0, go);
+                    ptx::mma_ts1(kTmS, kTmW + 16 + 8 * ks, dd + 128 * ks, id128t, 1, go);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    ptx::mma_ts1(kTmP, kTmU + 8 * ks, dt + kP + 2 * ks, id64, ks > 0, go);
+                if (!wait(kbU + 1, c)) return false;
+#pragma unroll
+                for (int hk = 0; hk < 2; ++hk) {
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        const uint32_t k = dd + hk * kImage + 128 * (2 + ks);
+                        ptx::mma_ts1(kTmS + 64 * hk, kTmW + 32 + 8 * ks, k, id64t, 1, go);
+                        ptx::mma_ts1(kTmS + 64 * hk, kTmW + 48 + 8 * ks, k, id64t, 1, go);
+                    }
+                    ptx::mma_commit1(&bars[kbDDone + hk], go);
+                }
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    ptx::mma_ts1(kTmP + 32, kTmU + 32 + 8 * ks, dt + kP + kHalfRows + 4 + 2 * ks, id32, 1, go);
                 ptx::mma_commit1(&bars[kbPDone], go);
+                return true;
+            };
+            for (int c = 0; c < nc; c += kStages) {
+                if (!chunk(std::integral_constant<int, 0>{}, c)) break;
+                if (c + 1 < nc && !chunk(std::integral_constant<int, 1>{}, c + 1)) break;
+                if (c + 2 < nc && !chunk(std::integral_constant<int, 2>{}, c + 2)) break;
             }
             ptx::mma_commit1(&bars[kbDrain], go);
             __syncwarp();
@@ -654,11 +708,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
         // ---------------- outputs: a warp's 32 lanes (value columns), read as fragments of 16 x 8 ----------------
         const int w = warp & 3, col0 = 32 * w;
         const uint32_t tl = tmem + ((uint32_t)col0 << 16);
-        const int64_t step = (int64_t)a.HV * kGdnDim;
-        uint16_t* out = a.out + (int64_t)b * a.n * step + h * kGdnDim;
-        // stmatrix: this lane's row (a token, within two groups of 8) and 8 columns
-        const int st_off = ((lane & 7) + ((lane >> 4) << 3)) * kVRow + (col0 + ((lane >> 3) & 1) * 8) * 2;
-        for (int c = 0; c < nc; ++c, out += kC * step) {
+        // stmatrix: this lane's row (a token, within two groups of 8) in the swizzled image of its 64 columns
+        const int st_row = ((lane & 7) + ((lane >> 4) << 3)) * 128 + (w >> 1) * kTile;
+        const int st_piece = (w & 1) * 4 + ((lane >> 3) & 1);
+        for (int c = 0; c < nc; ++c) {
             const int st = c % kStages;
             uint8_t* stage = smem + st * kStageBytes;
             const float* scal = reinterpret_cast<const float*>(stage + kStageTP + kOffScal);
@@ -699,41 +752,71 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                             o[2 * j + r] = pack_bf16(v.x, v.y);
                         }
                     }
-                    const uint32_t to = ptx::smem_u32(stage + kStageV) + st_off + 32 * p * kVRow + 32 * hl;
+                    const uint32_t to = ptx::smem_u32(stage + kStageV) + st_row + 32 * p * 128 +
+                                        (((st_piece + 2 * hl) ^ (lane & 7)) << 4);
                     stsm4_trans(to, o[0], o[1], o[2], o[3]);
-                    stsm4_trans(to + 16 * kVRow, o[4], o[5], o[6], o[7]);
+                    stsm4_trans(to + 16 * 128, o[4], o[5], o[6], o[7]);
                 }
             }
             ptx::fence_proxy_async_smem();
-            ptx::named_bar_sync(5, 128);
-            const int t = 16 * w + lane;                // a row (256 bytes) a lane
-            if (lane < 16 && t < left) {
-                bulk_store(out + t * step, stage + kStageV + t * kVRow, kGdnDim * 2);
-                ptx::bulk_commit();
-                ptx::bulk_wait_read_all();
+            ptx::named_bar_sync(kBarOut, 128);
+            if (left >= kC) {
+                if (warp == kWarpOut && lane < 2) {
+                    tma_store_2d(&maps.out, stage + kStageV + lane * kTile, h * kGdnDim + 64 * lane, b * a.n + c * kC);
+                    ptx::bulk_commit();
+                    ptx::bulk_wait_read_all();
+                }
+            } else {   // the last chunk: rows past the sequence's end stay as they are
+                for (int i = tid - 32 * kWarpOut; i < 16 * left; i += 128) {
+                    const int t = i >> 4, piece = i & 15;
+                    const uint4 x = *reinterpret_cast<const uint4*>(stage + kStageV + (piece >> 3) * kTile + piece_at(t, piece & 7));
+                    *reinterpret_cast<uint4*>(a.out + (((int64_t)b * a.n + c * kC + t) * a.HV + h) * kGdnDim + 8 * piece) = x;
+                }
             }
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);
+            if (warp == kWarpOut && lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);
         }
     } else {
         regs_up<kRegsMain>();
         // ---------------- a thread: lane (value column) `row`, half `wg` of the keys or tokens ----------------
-        const int wg = warp >> 2, row = 32 * (warp & 3) + lane;
-        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const int pair_bar = 1 + (warp & 3);
+        // The halves run one behind the other, so that one's arithmetic covers the other's products.
+        const int wg = warp >> 2, w = warp & 3, row = 32 * w + lane;
+        const uint32_t tl = tmem + ((uint32_t)(32 * w) << 16);
         auto signal = [&](int bar) {
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars[bar]);
+            if (lane == 0) ptx::mbar_arrive(&bars[bar + wg]);
         };
-        // the larger of the two halves' values, of this lane's state and V
-        auto exchange = [&](float& ms, float& mv) {
+        // this half's largest values of the lane's state and V, offered to the other half and taken from it
+        auto offer = [&](float ms, float mv) {
             maxima[wg * 128 + row] = ms;
             maxima[(2 + wg) * 128 + row] = mv;
-            ptx::named_bar_sync(pair_bar, 64);
+            ptx::named_bar_arrive(kBarPair + 4 * wg + w, 64);
+        };
+        auto take = [&](float& ms, float& mv) {
+            ptx::named_bar_sync(kBarPair + 4 * (wg ^ 1) + w, 64);
             ms = fmaxf(ms, maxima[(wg ^ 1) * 128 + row]);
             mv = fmaxf(mv, maxima[(2 + (wg ^ 1)) * 128 + row]);
+        };
+        // this half's V rows of chunk c
+        f2 v[16];
+        auto get_v = [&](int c) {
+            const uint16_t* vs = reinterpret_cast<const uint16_t*>(smem + (c % kStages) * kStageBytes + kStageV) + 32 * wg * kGdnDim + row;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = pack2(bf16_float(vs[2 * i * kGdnDim]), bf16_float(vs[(2 * i + 1) * kGdnDim]));
+            const int left = len - c * kC - 32 * wg;
+            if (left < 32) {   // tokens past the end, whatever stands there (their K is 0, so their X will be)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 d = unpack2(v[i]);
+                    v[i] = pack2(2 * i < left ? d.x : 0.f, 2 * i + 1 < left ? d.y : 0.f);
+                }
+            }
+            float m[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m[i & 1] = absmax(m[i & 1], v[i]);
+            return fmaxf(m[0], m[1]);
         };
         // The lane's scales are powers of two from bounds on its values, all known before the products they
         // are for: of the state at the start (its own maximum), of X (V and the keys' sums), of U and the
@@ -741,15 +824,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
         f2 S[32];   // times 2^es: keys 64 wg + 2 i, 2 i + 1
         int es;
         float* gs = a.state + ((int64_t)unit * kGdnDim + 64 * wg) * kGdnDim + row;
+        float smax = 0.f, vmax;
         {
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = pack2(gs[2 * i * kGdnDim], gs[(2 * i + 1) * kGdnDim]);
-            float ms = 0.f, none = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ms = absmax(ms, S[i]);
-            exchange(ms, none);
-            ptx::named_bar_sync(pair_bar, 64);   // both have read, before the first chunk's exchange
-            es = scale_exponent(ms, 15);
+            for (int i = 0; i < 32; ++i) smax = absmax(smax, S[i]);
+            ok = ptx::mbar_wait_warp(&bars[kbFull], 0, abort_flag, a.status);
+            vmax = get_v(0);
+            offer(smax, vmax);
+            take(smax, vmax);
+            es = scale_exponent(smax, 15);
+            smax *= pow2(es);   // scaled, as the state is
             const f2 f = pack2(pow2(es), pow2(es));
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = mul2(S[i], f);
@@ -761,8 +847,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                 uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) split2(S[16 * p + i], hi[i], lo[i]);
-                ptx::tmem_st16(tl + kTmS + 32 * wg + 16 * p, hi);
-                ptx::tmem_st16(tl + kTmS + 64 + 32 * wg + 16 * p, lo);
+                ptx::tmem_st16(tl + kTmS + 64 * wg + 16 * p, hi);
+                ptx::tmem_st16(tl + kTmS + 64 * wg + 32 + 16 * p, lo);
             }
             signal(kbS);
         };
@@ -770,32 +856,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
         put_state(0);
         for (int c = 0; c < nc; ++c) {
             const int st = c % kStages;
-            const uint8_t* stage = smem + st * kStageBytes;
-            const float* one = reinterpret_cast<const float*>(stage + kStageTP + kOffScal);
+            const float* one = reinterpret_cast<const float*>(smem + st * kStageBytes + kStageTP + kOffScal);
             const float* scal = one + 32 * wg;   // this half's tokens
-            const uint16_t* vs = reinterpret_cast<const uint16_t*>(stage + kStageV + 32 * wg * kVRow) + row;
-            const int left = len - c * kC - 32 * wg;   // tokens of this half
-            // (an abandoned CTA goes on through its barriers, on values that nobody uses)
-            ok = ptx::mbar_wait_warp(&bars[kbFull + st], (c / kStages) & 1, abort_flag, a.status) && ok;
-            // while W is computed: V, the bounds and the scales
-            uint32_t x[32];
-            f2 v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = pack2(bf16_float(vs[i * kVRow]), bf16_float(vs[i * kVRow + kVRow / 2]));
-            if (left < 32) {   // tokens past the end: whatever the stage held there (their K is 0, so their X will be)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 d = unpack2(v[i]);
-                    v[i] = pack2(2 * i < left ? d.x : 0.f, 2 * i + 1 < left ? d.y : 0.f);
-                }
-            }
-            float ms[2] = {0.f, 0.f}, mv[2] = {0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ms[i & 1] = absmax(ms[i & 1], S[i]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mv[i & 1] = absmax(mv[i & 1], v[i]);
-            float smax = fmaxf(ms[0], ms[1]), vmax = fmaxf(mv[0], mv[1]);
-            exchange(smax, vmax);
+            // while W is computed: the bounds and the scales
+            if (c > 0) take(smax, vmax);
             const float inv_s = pow2(-es);
             smax *= inv_s;
             const float keep = one[kEC], bx = fmaf(one[kBW], smax, vmax);
@@ -806,13 +870,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             const float cu = fminf(pow2(eu) * from_x, kCap);          // U's accumulator to U's scale
             const float cd = fminf(pow2(es1) * from_x, kCap);         // and, with c3, to the new state's
             const float ck = fminf(keep * inv_s * pow2(es1), kCap);   // the state to its new scale
+            if (wg == 0) exps[(c & 1) * 256 + 128 + row] = (int8_t)eu;
             {
                 const f2 f = pack2(fx, fx);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) v[i] = mul2(v[i], f);
             }
             // X
-            ok = ptx::mbar_wait_warp(&bars[kbWDone], c & 1, abort_flag, a.status) && ok;
+            // (an abandoned CTA goes on through its barriers, on values that nobody uses)
+            uint32_t x[32];
+            ok = ptx::mbar_wait_warp(&bars[kbWDone + wg], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmW + 32 * wg, x);
             ptx::tmem_wait_ld();
@@ -827,13 +894,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                     for (int j = 0; j < 2; ++j)
                         split2(fma2(pack2(x[2 * (i + j)], x[2 * (i + j) + 1]), mul2(c1[j], cw2), v[i + j]), hi[i + j], lo[i + j]);
                 }
-                ptx::tmem_st16(tl + kTmX + 16 * wg, hi);
-                ptx::tmem_st16(tl + kTmX + 32 + 16 * wg, lo);
+                ptx::tmem_st16(tl + kTmX + 32 * wg, hi);
+                ptx::tmem_st16(tl + kTmX + 32 * wg + 16, lo);
                 signal(kbX);
             }
             // U, and U scaled for the state
-            if (wg == 0) exps[(c & 1) * 256 + 128 + row] = (int8_t)eu;
-            ok = ptx::mbar_wait_warp(&bars[kbUDone], c & 1, abort_flag, a.status) && ok;
+            ok = ptx::mbar_wait_warp(&bars[kbUDone + wg], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmU + 32 * wg, x);
             ptx::tmem_wait_ld();
@@ -847,40 +913,53 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const f2 y = pack2(x[2 * (i + j)], x[2 * (i + j) + 1]);
-                        const float2 w = unpack2(mul2(y, cu2));
-                        u[i + j] = half2_bits(w.x, w.y);
+                        const float2 z = unpack2(mul2(y, cu2));
+                        u[i + j] = half2_bits(z.x, z.y);
                         split2(mul2(y, mul2(c3[j], cd2)), hi[i + j], lo[i + j]);
                     }
                 }
-                ptx::tmem_st16(tl + kTmX + 16 * wg, hi);
-                ptx::tmem_st16(tl + kTmX + 32 + 16 * wg, lo);
-                ptx::tmem_st16(tl + kTmUh + 16 * wg, u);
+                ptx::tmem_st16(tl + kTmW + 32 * wg, hi);
+                ptx::tmem_st16(tl + kTmW + 32 * wg + 16, lo);
+                ptx::tmem_st16(tl + kTmU + 32 * wg, u);
                 signal(kbU);
             }
             if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);   // (the output warps wait for the products)
+            // while the increment is computed: the next chunk's V
+            if (c + 1 < nc) {
+                ok = ptx::mbar_wait_warp(&bars[kbFull + (c + 1) % kStages], ((c + 1) / kStages) & 1, abort_flag, a.status) && ok;
+                vmax = get_v(c + 1);
+            }
             // the state
-            ok = ptx::mbar_wait_warp(&bars[kbDDone], c & 1, abort_flag, a.status) && ok;
+            ok = ptx::mbar_wait_warp(&bars[kbDDone + wg], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             es = es1;
             {
                 const f2 k2 = pack2(ck, ck);
+                float m[2] = {0.f, 0.f};
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    ptx::tmem_ld32(tl + kTmD + 64 * wg + 32 * p, x);
+                    ptx::tmem_ld32(tl + kTmS + 64 * wg + 32 * p, x);
                     ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) S[16 * p + i] = fma2(S[16 * p + i], k2, pack2(x[2 * i], x[2 * i + 1]));
+                    for (int i = 0; i < 16; ++i) {
+                        S[16 * p + i] = fma2(S[16 * p + i], k2, pack2(x[2 * i], x[2 * i + 1]));
+                        m[i & 1] = absmax(m[i & 1], S[16 * p + i]);
+                    }
                 }
+                smax = fmaxf(m[0], m[1]);
             }
-            if (c + 1 < nc) put_state(c + 1);
+            if (c + 1 < nc) {
+                offer(smax, vmax);
+                put_state(c + 1);
+            }
         }
         if (ok) {
             const float f = pow2(-es);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                const float2 x = unpack2(S[i]);
-                gs[2 * i * kGdnDim] = x.x * f;
-                gs[(2 * i + 1) * kGdnDim] = x.y * f;
+                const float2 y = unpack2(S[i]);
+                gs[2 * i * kGdnDim] = y.x * f;
+                gs[(2 * i + 1) * kGdnDim] = y.y * f;
             }
         }
     }
@@ -888,6 +967,19 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == kWarpMma) ptx::tmem_dealloc1(tmem, kTmCols);
+}
+
+// A 2-D BF16 tensor of `rows` rows of `cols` values, boxes of bc columns x 64 rows.
+bool make_map2(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t bc, CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols * 2};
+    const cuuint32_t box[2] = {bc, kC};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -910,11 +1002,16 @@ cudaError_t launch_gdn_prefill(const DeltaArgs& a, cudaStream_t stream) {
     cudaError_t e = prep_limit.ensure(prep_smem);
     if (e == cudaSuccess) e = scan_limit.ensure(kScanSmem);
     if (e != cudaSuccess) return e;
+    ScanMaps maps;
+    const uint64_t rows = (uint64_t)a.B * a.n;
+    if (!make_map2(&maps.v, a.qkv, a.C, rows, kGdnDim, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !make_map2(&maps.out, a.out, (uint64_t)a.HV * kGdnDim, rows, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
     PdlLaunch prep((unsigned)grid, kPrepThreads, prep_smem, stream);
     e = cudaLaunchKernelEx(&prep.cfg, gdn_prep_kernel, a, NC);
     if (e != cudaSuccess) return e;
     PdlLaunch scan((unsigned)(a.B * a.HV), kScanThreads, kScanSmem, stream);
-    return cudaLaunchKernelEx(&scan.cfg, gdn_scan_kernel, a, NC);
+    return cudaLaunchKernelEx(&scan.cfg, gdn_scan_kernel, a, maps, NC);
 }
 
 }  // namespace rma

@@ -1,6 +1,7 @@
 // Internal declarations shared by the librma translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -141,6 +142,12 @@ cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t stream);
 // Quantise every row of `src` (BF16) into `dst` (FP8), one layer at a time; scores and counters copied.
 cudaError_t launch_quantize_layer(const LayerView& dst, const LayerView& src, cudaStream_t stream);
 size_t prefill_workspace_bytes(const rma_config& cfg, int n_tok);
+
+// cuTensorMapEncodeTiled through the driver entry point, or null.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled_fn();
 
 // ---- the layers around RMA attention (rma_qk_norm_rope, rma_gdn_*) ----
 
