@@ -105,20 +105,145 @@ __device__ __forceinline__ int piece_at(int row, int piece) { return row * 128 +
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
 constexpr int kHeadsAtOnce = 8;    // value heads whose gates are computed together, one per warp
+constexpr int kLd = kC + 4;        // row of a matrix that the tensor cores' fragments are read from
+constexpr int kLdY = 12;
 
+// Two groups of four warps, each with a value head of its own at a time.
 struct __align__(1024) PrepSmem {
-    uint8_t kq[kKQBytes];
-    float A[kC][kC + 1];
-    float T[kC][kC + 1];
-    float Y[32][33];
-    double G[kHeadsAtOnce][kC];
+    union {
+        uint8_t kq[kKQBytes];           // operand images of K and Q
+        float prod[2][kC][kC];          // then K K^T and Q K^T, 16-byte pieces permuted (prod_at)
+    };
+    float T[2][kC][kLd];                // A, overwritten by its inverse block by block
+    float Y[2][4][32][kLdY];            // a warp's intermediate products
+    float Gh[kHeadsAtOnce][kC], Gl[kHeadsAtOnce][kC];   // sums of g, as the sum of two floats
     float beta[kHeadsAtOnce][kC];
-    float rk[kC], rq[kC], ks[kC];   // row factors of K and Q, sums of |K|
-    float c1[kC], c3[kC], tsum[kC];
-    uint32_t pmax, tmax;            // largest |P| and |T| (float bits)
+    float rk[kC], rq[kC], ks[kC];       // row factors of K and Q, sums of |K|
+    float kn[kC], qn[kC];               // norms of the rows with their factors
+    float tsum[2][kC], c1[2][kC], c3[2][kC];
+    uint32_t tmax[2];
 };
 
-__global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
+__device__ __forceinline__ int prod_at(int row, int col) {
+    return row * kC + ((((col >> 2) ^ ((row & 7) << 1)) << 2) | (col & 3));
+}
+
+// TF32 with FP32's precision: a value as hi + lo, products without lo x lo (2^-22)
+struct Tf {
+    uint32_t hi, lo;
+};
+__device__ __forceinline__ Tf tf_split(float x) {
+    Tf t;
+    asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(t.hi) : "f"(x));
+    asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(t.lo) : "f"(x - __uint_as_float(t.hi)));
+    return t;
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d += A[16 x 8] B[8 x 8], A's rows lda floats apart, B's ldb
+__device__ __forceinline__ void mma_fp32(float (&d)[4], const float* A, int lda, const float* B, int ldb, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const Tf a0 = tf_split(A[r * lda + c]), a1 = tf_split(A[(r + 8) * lda + c]);
+    const Tf a2 = tf_split(A[r * lda + c + 4]), a3 = tf_split(A[(r + 8) * lda + c + 4]);
+    const Tf b0 = tf_split(B[c * ldb + r]), b1 = tf_split(B[(c + 4) * ldb + r]);
+    mma_tf32(d, a0.lo, a1.lo, a2.lo, a3.lo, b0.hi, b1.hi);
+    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, b0.lo, b1.lo);
+    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, b0.hi, b1.hi);
+}
+
+// T = (1 + A)^-1 in place, A strictly lower triangular 64 x 64 (zeros elsewhere); the group's four warps.
+//   Diagonal blocks of 16 by substitution, a lane per column; then pairs of blocks twice over,
+//   T21 = -T22 A21 T11, on the tensor cores: to 32 by a warp each, to 64 by all four, 8 columns each.
+__device__ __forceinline__ void invert(float (*T)[kLd], float (*Y)[32][kLdY], int warp, int lane, int bar) {
+    if (warp < 2) {
+        const int o = 32 * warp;
+        {
+            const int q = o + (lane & 16), j = lane & 15;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
+#pragma unroll
+            for (int l = 0; l < 15; ++l)
+#pragma unroll
+                for (int i = l + 1; i < 16; ++i) x[i] = fmaf(-T[q + i][q + l], x[l], x[i]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) T[q + i][q + j] = x[i];
+            __syncwarp();
+        }
+        float* y = &Y[warp][0][0];   // 16 x 16, rows 20 apart (within the warp's 32 x 12)
+        const int r = lane >> 2, c = 2 * (lane & 3);
+        float d[2][4] = {};
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int ks = nt; ks < 2; ++ks)   // T11's columns 8 nt .. are 0 above row 8 nt
+                mma_fp32(d[nt], &T[o + 16][o + 8 * ks], kLd, &T[o + 8 * ks][o + 8 * nt], kLd, lane);
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            y[r * 20 + 8 * nt + c] = d[nt][0];
+            y[r * 20 + 8 * nt + c + 1] = d[nt][1];
+            y[(r + 8) * 20 + 8 * nt + c] = d[nt][2];
+            y[(r + 8) * 20 + 8 * nt + c + 1] = d[nt][3];
+        }
+        __syncwarp();
+        float e[2][4] = {};
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+                mma_fp32(e[nt], &T[o + 16][o + 16 + 8 * ks], kLd, y + 8 * ks * 20 + 8 * nt, 20, lane);
+        __syncwarp();
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            float* t = &T[o + 16 + r][o + 8 * nt + c];
+            t[0] = -e[nt][0];
+            t[1] = -e[nt][1];
+            t[8 * kLd] = -e[nt][2];
+            t[8 * kLd + 1] = -e[nt][3];
+        }
+    }
+    ptx::named_bar_sync(bar, 128);
+    {
+        const int n0 = 8 * warp, r = lane >> 2, c = 2 * (lane & 3);
+        float d[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+            if (ks >= warp)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) mma_fp32(d[mt], &T[32 + 16 * mt][8 * ks], kLd, &T[8 * ks][n0], kLd, lane);
+        float* y = &Y[warp][0][0];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            y[(16 * mt + r) * kLdY + c] = d[mt][0];
+            y[(16 * mt + r) * kLdY + c + 1] = d[mt][1];
+            y[(16 * mt + r + 8) * kLdY + c] = d[mt][2];
+            y[(16 * mt + r + 8) * kLdY + c + 1] = d[mt][3];
+        }
+        ptx::named_bar_sync(bar, 128);   // A21 has been read
+        float e[2][4] = {};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+                if (ks < 2 * mt + 2) mma_fp32(e[mt], &T[32 + 16 * mt][32 + 8 * ks], kLd, y + 8 * ks * kLdY, kLdY, lane);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+            float* t = &T[32 + 16 * mt + r][n0 + c];
+            t[0] = -e[mt][0];
+            t[1] = -e[mt][1];
+            t[8 * kLd] = -e[mt][2];
+            t[8 * kLd + 1] = -e[mt][3];
+        }
+    }
+    ptx::named_bar_sync(bar, 128);
+}
+
+__global__ void __launch_bounds__(kPrepThreads, 2) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
     extern __shared__ uint8_t smem_raw[];
     PrepSmem& s = *reinterpret_cast<PrepSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -132,19 +257,60 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
     const int valid = min(len - t0, kC);
     if (valid <= 0) return;
     const int R = a.HV / a.HK;
+    uint8_t* kq_out = a.ws + (((int64_t)b * a.HK + kh) * NC + c) * kKQBytes;
+    uint8_t* tp_base = a.ws + (int64_t)a.B * a.HK * NC * kKQBytes;
+
+    // gates of up to 8 value heads from r0, a warp each: two tokens a lane, running sums in FP64
+    auto head_gates = [&](int r0) {
+        if (r0 + warp >= R) return;
+        const int h = kh * R + r0 + warp;
+        const float alpha = expf(a.a_log[h]), dt = a.dt_bias[h];
+        float g[2], bt[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = 2 * lane + i;
+            g[i] = 0.f;
+            bt[i] = 0.f;
+            if (t < valid) {
+                const int64_t at = ((int64_t)b * a.n + t0 + t) * a.ab_stride + h;
+                gates(a.a[at], a.b[at], alpha, dt, g[i], bt[i]);
+            }
+        }
+        const double own = (double)g[0] + (double)g[1];
+        double run = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double up = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += up;
+        }
+        const double G[2] = {run - own + (double)g[0], run};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float hi = (float)G[i];
+            s.Gh[warp][2 * lane + i] = hi;
+            s.Gl[warp][2 * lane + i] = (float)(G[i] - (double)hi);
+            s.beta[warp][2 * lane + i] = bt[i];
+        }
+    };
 
     // K and Q rows into FP16 images, a half-warp per row, with the row's norm
     {
         const int sub = lane >> 4, l16 = lane & 15;
+        uint4 raw[8];
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const int row = (it & 3) * 16 + warp * 2 + sub;
+            raw[it] = make_uint4(0, 0, 0, 0);
+            if (row < valid)
+                raw[it] = *reinterpret_cast<const uint4*>(a.qkv + ((int64_t)b * a.n + t0 + row) * a.C +
+                                                          ((it >> 2) ? kh : a.HK + kh) * kGdnDim + 8 * l16);
+        }
+        head_gates(0);
 #pragma unroll
         for (int it = 0; it < 8; ++it) {
             const int m = it >> 2;                                    // 0: K, 1: Q
             const int row = (it & 3) * 16 + warp * 2 + sub;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (row < valid)
-                raw = *reinterpret_cast<const uint4*>(a.qkv + ((int64_t)b * a.n + t0 + row) * a.C +
-                                                      (m ? kh : a.HK + kh) * kGdnDim + 8 * l16);
-            const float2 p0 = unpack_bf16(raw.x), p1 = unpack_bf16(raw.y), p2 = unpack_bf16(raw.z), p3 = unpack_bf16(raw.w);
+            const float2 p0 = unpack_bf16(raw[it].x), p1 = unpack_bf16(raw[it].y), p2 = unpack_bf16(raw[it].z), p3 = unpack_bf16(raw[it].w);
             float x[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
             float mx = 0.f;
 #pragma unroll
@@ -165,8 +331,10 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                 ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 sa += __shfl_xor_sync(0xffffffffu, sa, o);
             }
-            *reinterpret_cast<uint4*>(s.kq + (2 * m + (l16 >> 3)) * kTile + piece_at(row, l16 & 7)) =
-                make_uint4(half2_bits(x[0], x[1]), half2_bits(x[2], x[3]), half2_bits(x[4], x[5]), half2_bits(x[6], x[7]));
+            const int at = (2 * m + (l16 >> 3)) * kTile + piece_at(row, l16 & 7);
+            const uint4 v = make_uint4(half2_bits(x[0], x[1]), half2_bits(x[2], x[3]), half2_bits(x[4], x[5]), half2_bits(x[6], x[7]));
+            *reinterpret_cast<uint4*>(s.kq + at) = v;
+            *reinterpret_cast<uint4*>(kq_out + at) = v;
             if (l16 == 0) {
                 // 1 / sqrt(sum x^2 + eps) times the row's scale; the sum is of scaled values, so the one
                 // form keeps large rows from overflowing and the other rows far below eps from NaN
@@ -176,26 +344,28 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                     else r = inv / sqrtf(ss * inv * inv + a.l2_eps);
                 }
                 if (row >= valid) r = 0.f;
-                if (m) s.rq[row] = r * a.scale;
-                else s.rk[row] = r, s.ks[row] = sa;
+                if (m) {
+                    r *= a.scale;
+                    s.rq[row] = r;
+                    s.qn[row] = fabsf(r) * sqrtf(ss);
+                } else {
+                    s.rk[row] = r;
+                    s.ks[row] = sa;
+                    s.kn[row] = r * sqrtf(ss);
+                }
             }
         }
     }
     __syncthreads();
-    // the images to the workspace
-    uint8_t* kq_out = a.ws + (((int64_t)b * a.HK + kh) * NC + c) * kKQBytes;
-    for (int i = tid; i < kKQBytes / 16; i += kPrepThreads)
-        reinterpret_cast<uint4*>(kq_out)[i] = reinterpret_cast<const uint4*>(s.kq)[i];
-    uint8_t* tp_base = a.ws + (int64_t)a.B * a.HK * NC * kKQBytes;
 
-    // rows 16 rb .. + 15 of K K^T (warps 0-3) or Q K^T (warps 4-7): acc[nt] = columns 8 nt ..
-    const int rb = warp & 3, m = warp >> 2;
-    float acc[8][4];
-#pragma unroll
-    for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+    // rows 16 rb .. + 15 of K K^T (warps 0-3) or Q K^T (warps 4-7), up to the diagonal block
     {
+        const int rb = warp & 3, m = warp >> 2;
+        float acc[8][4];
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
         const uint32_t kbase = ptx::smem_u32(s.kq), abase = kbase + 2 * m * kTile;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
@@ -203,7 +373,7 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
             ldsm4(abase + (ks >> 2) * kTile + piece_at(16 * rb + (lane & 15), (ks & 3) * 2 + (lane >> 4)), fa);
 #pragma unroll
             for (int np = 0; np < 4; ++np) {
-                if (np <= rb) {   // columns above the diagonal block are not used
+                if (np <= rb) {
                     uint32_t fb[4];
                     ldsm4(kbase + (ks >> 2) * kTile +
                               piece_at(16 * np + (lane & 7) + ((lane >> 4) << 3), (ks & 3) * 2 + ((lane >> 3) & 1)), fb);
@@ -212,212 +382,133 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                 }
             }
         }
-    }
-
-    for (int r0 = 0; r0 < R; r0 += kHeadsAtOnce) {
-        // gates of up to 8 value heads, a warp each: two tokens a lane, running sums in FP64
-        __syncthreads();
-        if (r0 + warp < R) {
-            const int h = kh * R + r0 + warp;
-            const float alpha = expf(a.a_log[h]), dt = a.dt_bias[h];
-            float g[2], bt[2];
+        __syncthreads();   // the images have been read
+        float* prod = &s.prod[m][0][0];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int t = 2 * lane + i;
-                g[i] = 0.f;
-                bt[i] = 0.f;
-                if (t < valid) {
-                    const int64_t at = ((int64_t)b * a.n + t0 + t) * a.ab_stride + h;
-                    gates(a.a[at], a.b[at], alpha, dt, g[i], bt[i]);
-                }
-            }
-            const double own = (double)g[0] + (double)g[1];
-            double run = own;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const double up = __shfl_up_sync(0xffffffffu, run, o);
-                if (lane >= o) run += up;
-            }
-            s.G[warp][2 * lane] = run - own + (double)g[0];
-            s.G[warp][2 * lane + 1] = run;
-            s.beta[warp][2 * lane] = bt[0];
-            s.beta[warp][2 * lane + 1] = bt[1];
+        for (int nt = 0; nt < 8; ++nt) {
+            const int row = 16 * rb + (lane >> 2), col = 8 * nt + 2 * (lane & 3);
+            *reinterpret_cast<float2*>(prod + prod_at(row, col)) = make_float2(acc[nt][0], acc[nt][1]);
+            *reinterpret_cast<float2*>(prod + prod_at(row + 8, col)) = make_float2(acc[nt][2], acc[nt][3]);
         }
-        for (int r = r0; r < min(r0 + kHeadsAtOnce, R); ++r) {
-            if (tid == 0) s.pmax = 0u;
+    }
+    // P is scaled by its bound, the largest norms of Q and K
+    float pmax;
+    {
+        float q = fmaxf(s.qn[lane], s.qn[lane + 32]), k = fmaxf(s.kn[lane], s.kn[lane + 32]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            q = fmaxf(q, __shfl_xor_sync(0xffffffffu, q, o));
+            k = fmaxf(k, __shfl_xor_sync(0xffffffffu, k, o));
+        }
+        pmax = q * k;
+    }
+    const int ep = scale_exponent(pmax, 8);
+    const float p_scale = pow2(ep);
+    __syncthreads();
+
+    const int grp = warp >> 2, gt = tid & 127, gw = warp & 3, bar = 1 + grp;
+    for (int r0 = 0; r0 < R; r0 += kHeadsAtOnce) {
+        if (r0 > 0) {
             __syncthreads();
-            if (tid == 0) s.tmax = 0u;
-            const double* G = s.G[r - r0];
-            const float* beta = s.beta[r - r0];
+            head_gates(r0);
+            __syncthreads();
+        }
+        for (int r = r0 + grp; r < min(r0 + kHeadsAtOnce, R); r += 2) {
+            const float *Gh = s.Gh[r - r0], *Gl = s.Gl[r - r0], *beta = s.beta[r - r0];
             uint8_t* out = tp_base + (((int64_t)b * a.HV + kh * R + r) * NC + c) * kTPBytes;
             float* scal = reinterpret_cast<float*>(out + kOffScal);
-            const int i0 = 16 * rb + (lane >> 2);
-            float p[32];
-            if (m == 0) {
-                // A, strictly below the diagonal
+            float (*T)[kLd] = s.T[grp];
+            // A (strictly below the diagonal) and P, eight columns of a row at a time
+            const int p = gt & 7;
+            float Gjh[8], Gjl[8], rkj[8];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int i = i0 + 8 * half;
-                    const double Gi = G[i];
-                    const float f = beta[i] * s.rk[i];
+            for (int x = 0; x < 8; ++x) {
+                Gjh[x] = Gh[8 * p + x];
+                Gjl[x] = Gl[8 * p + x];
+                rkj[x] = s.rk[8 * p + x];
+            }
 #pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
+            for (int k = 0; k < 4; ++k) {
+                const int i = (gt >> 3) + 16 * k;
+                float A[8], P[8];
+                if (8 * p <= i) {
+                    const float4 k0 = *reinterpret_cast<const float4*>(&s.prod[0][0][0] + prod_at(i, 8 * p));
+                    const float4 k1 = *reinterpret_cast<const float4*>(&s.prod[0][0][0] + prod_at(i, 8 * p + 4));
+                    const float4 q0 = *reinterpret_cast<const float4*>(&s.prod[1][0][0] + prod_at(i, 8 * p));
+                    const float4 q1 = *reinterpret_cast<const float4*>(&s.prod[1][0][0] + prod_at(i, 8 * p + 4));
+                    const float kk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+                    const float qk[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                    const float gh = Gh[i], gl = Gl[i], fa = beta[i] * s.rk[i], fp = s.rq[i] * p_scale;
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int j = 8 * nt + 2 * (lane & 3) + x;
-                            float v = 0.f;
-                            if (j < i) v = f * s.rk[j] * __expf((float)(Gi - G[j])) * acc[nt][2 * half + x];
-                            s.A[i][j] = v;
-                        }
+                    for (int x = 0; x < 8; ++x) {
+                        const int j = 8 * p + x;
+                        const float d = rkj[x] * __expf((gh - Gjh[x]) + (gl - Gjl[x]));
+                        A[x] = j < i ? fa * d * kk[x] : 0.f;
+                        P[x] = j <= i ? fp * d * qk[x] : 0.f;
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) A[x] = P[x] = 0.f;
                 }
-                if (tid < kC) {
-                    const float since = __expf((float)G[tid]), until = __expf((float)(G[kC - 1] - G[tid]));
-                    scal[kC1 + tid] = s.c1[tid] = since * s.rk[tid];
-                    scal[kC2 + tid] = since * s.rq[tid];
-                    scal[kC3 + tid] = s.c3[tid] = until * s.rk[tid];
-                }
-            } else {
-                // P, and its largest
-                float mx = 0.f;
+                *reinterpret_cast<float4*>(&T[i][8 * p]) = make_float4(A[0], A[1], A[2], A[3]);
+                *reinterpret_cast<float4*>(&T[i][8 * p + 4]) = make_float4(A[4], A[5], A[6], A[7]);
+                *reinterpret_cast<uint4*>(out + kOffP + piece_at(i, p)) =
+                    make_uint4(half2_bits(P[0], P[1]), half2_bits(P[2], P[3]), half2_bits(P[4], P[5]), half2_bits(P[6], P[7]));
+            }
+            if (gt < kC) {
+                const float since = __expf(Gh[gt] + Gl[gt]);
+                const float until = __expf((Gh[kC - 1] - Gh[gt]) + (Gl[kC - 1] - Gl[gt]));
+                scal[kC1 + gt] = s.c1[grp][gt] = since * s.rk[gt];
+                scal[kC2 + gt] = since * s.rq[gt];
+                scal[kC3 + gt] = s.c3[grp][gt] = until * s.rk[gt];
+                if (gt == kC - 1) scal[kEC] = since;
+            }
+            if (gt == 0) s.tmax[grp] = 0u;
+            ptx::named_bar_sync(bar, 128);
+            invert(T, s.Y[grp], gw, lane, bar);
+            // T with beta's columns: its largest value, its rows' sums; scaled, split, to the workspace
+            {
+                float v[4][8], mx = 0.f;
+                const float4 b0 = *reinterpret_cast<const float4*>(beta + 8 * p), b1 = *reinterpret_cast<const float4*>(beta + 8 * p + 4);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int i = i0 + 8 * half;
-                    const double Gi = G[i];
-                    const float f = s.rq[i];
+                for (int k = 0; k < 4; ++k) {
+                    const int i = (gt >> 3) + 16 * k;
+                    const float4 t0 = *reinterpret_cast<const float4*>(&T[i][8 * p]), t1 = *reinterpret_cast<const float4*>(&T[i][8 * p + 4]);
+                    v[k][0] = t0.x * b0.x; v[k][1] = t0.y * b0.y; v[k][2] = t0.z * b0.z; v[k][3] = t0.w * b0.w;
+                    v[k][4] = t1.x * b1.x; v[k][5] = t1.y * b1.y; v[k][6] = t1.z * b1.z; v[k][7] = t1.w * b1.w;
+                    float sum = 0.f;
 #pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
+                    for (int x = 0; x < 8; ++x) {
+                        mx = fmaxf(mx, fabsf(v[k][x]));
+                        sum += fabsf(v[k][x]);
+                    }
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const int j = 8 * nt + 2 * (lane & 3) + x;
-                            float v = 0.f;
-                            if (j <= i) v = f * s.rk[j] * __expf((float)(Gi - G[j])) * acc[nt][2 * half + x];
-                            p[16 * half + 2 * nt + x] = v;
-                            mx = fmaxf(mx, fabsf(v));
-                        }
+                    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (p == 0) s.tsum[grp][i] = sum;
                 }
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                if (lane == 0) atomicMax(&s.pmax, __float_as_uint(mx));
-            }
-            __syncthreads();
-            if (m == 1) {
-                const int e = scale_exponent(__uint_as_float(s.pmax), 8);
+                if (lane == 0) atomicMax(&s.tmax[grp], __float_as_uint(mx));
+                ptx::named_bar_sync(bar, 128);
+                const int e = scale_exponent(__uint_as_float(s.tmax[grp]), 8);
                 const float sc = pow2(e);
-                if (tid == kPrepThreads - 1) {
-                    scal[kPS] = pow2(-e);
-                    scal[kEC] = __expf((float)G[kC - 1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = (gt >> 3) + 16 * k;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) split2(v[k][2 * x] * sc, v[k][2 * x + 1] * sc, hi[x], lo[x]);
+                    *reinterpret_cast<uint4*>(out + piece_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(out + kOffTLo + piece_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int nt = 0; nt < 8; ++nt)
-                        *reinterpret_cast<uint32_t*>(out + kOffP + piece_at(i0 + 8 * half, nt) + 4 * (lane & 3)) =
-                            half2_bits(p[16 * half + 2 * nt] * sc, p[16 * half + 2 * nt + 1] * sc);
-            }
-            // inverse of (1 + A): its four 16 x 16 diagonal blocks by substitution, a thread per column
-            if (tid < kC) {
-                const int o = tid & ~15, j = tid & 15;
-                float x[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = i == j ? 1.f : 0.f;
-#pragma unroll
-                for (int l = 0; l < 15; ++l)
-#pragma unroll
-                    for (int i = l + 1; i < 16; ++i) x[i] = fmaf(-s.A[o + i][o + l], x[l], x[i]);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s.T[o + i][o + j] = x[i];
-            }
-            __syncthreads();
-            // pairs of 16 into 32: T21 = -T22 (A21 T11)
-            {
-                const int o = (tid >> 7) * 32, i = (tid & 127) >> 3, j = (tid & 7) * 2;
-                float y0 = 0.f, y1 = 0.f;
-#pragma unroll
-                for (int l = 0; l < 16; ++l) {
-                    const float v = s.A[o + 16 + i][o + l];
-                    y0 = fmaf(v, s.T[o + l][o + j], y0);
-                    y1 = fmaf(v, s.T[o + l][o + j + 1], y1);
-                }
-                s.Y[(tid >> 7) * 16 + i][j] = y0;
-                s.Y[(tid >> 7) * 16 + i][j + 1] = y1;
-                // the quarter above the diagonal, which the next product reads
-                s.T[o + i][o + 16 + j] = 0.f;
-                s.T[o + i][o + 16 + j + 1] = 0.f;
-                __syncthreads();
-                float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-                for (int l = 0; l < 16; ++l) {
-                    const float v = s.T[o + 16 + i][o + 16 + l];
-                    z0 = fmaf(v, s.Y[(tid >> 7) * 16 + l][j], z0);
-                    z1 = fmaf(v, s.Y[(tid >> 7) * 16 + l][j + 1], z1);
-                }
-                s.T[o + 16 + i][o + j] = -z0;
-                s.T[o + 16 + i][o + j + 1] = -z1;
-            }
-            __syncthreads();
-            // and 32 into 64, 2 x 2 values a thread
-            {
-                const int i = (tid >> 4) * 2, j = (tid & 15) * 2;
-                float y[2][2] = {};
-#pragma unroll 8
-                for (int l = 0; l < 32; ++l) {
-                    const float u0 = s.A[32 + i][l], u1 = s.A[33 + i][l], v0 = s.T[l][j], v1 = s.T[l][j + 1];
-                    y[0][0] = fmaf(u0, v0, y[0][0]); y[0][1] = fmaf(u0, v1, y[0][1]);
-                    y[1][0] = fmaf(u1, v0, y[1][0]); y[1][1] = fmaf(u1, v1, y[1][1]);
-                }
-                __syncthreads();
-                s.Y[i][j] = y[0][0]; s.Y[i][j + 1] = y[0][1];
-                s.Y[i + 1][j] = y[1][0]; s.Y[i + 1][j + 1] = y[1][1];
-                s.T[i][32 + j] = s.T[i][33 + j] = s.T[i + 1][32 + j] = s.T[i + 1][33 + j] = 0.f;
-                __syncthreads();
-                float z[2][2] = {};
-#pragma unroll 8
-                for (int l = 0; l < 32; ++l) {
-                    const float u0 = s.T[32 + i][32 + l], u1 = s.T[33 + i][32 + l], v0 = s.Y[l][j], v1 = s.Y[l][j + 1];
-                    z[0][0] = fmaf(u0, v0, z[0][0]); z[0][1] = fmaf(u0, v1, z[0][1]);
-                    z[1][0] = fmaf(u1, v0, z[1][0]); z[1][1] = fmaf(u1, v1, z[1][1]);
-                }
-                s.T[32 + i][j] = -z[0][0]; s.T[32 + i][j + 1] = -z[0][1];
-                s.T[33 + i][j] = -z[1][0]; s.T[33 + i][j + 1] = -z[1][1];
-            }
-            __syncthreads();
-            // T with beta's columns, its largest value and its rows' sums: four threads a row, 16 columns each
-            {
-                const int i = tid >> 2, j0 = (tid & 3) * 16;
-                float v[16], mx = 0.f, sum = 0.f;
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                    v[x] = s.T[i][j0 + x] * beta[j0 + x];
-                    mx = fmaxf(mx, fabsf(v[x]));
-                    sum += fabsf(v[x]);
-                }
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                if ((tid & 3) == 0) s.tsum[i] = sum;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                if (lane == 0) atomicMax(&s.tmax, __float_as_uint(mx));
-                __syncthreads();
-                // scaled and split
-                const int e = scale_exponent(__uint_as_float(s.tmax), 8);
-                const float sc = pow2(e);
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x) split2(v[2 * x] * sc, v[2 * x + 1] * sc, hi[x], lo[x]);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const int at = piece_at(i, (j0 >> 3) + x);
-                    *reinterpret_cast<uint4*>(out + at) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-                    *reinterpret_cast<uint4*>(out + kOffTLo + at) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
-                }
-                if (warp == 0) {
+                if (gw == 0) {
                     float bw = 0.f, bt = 0.f, bs = 0.f;
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const int t = lane + 32 * x;
-                        bw = fmaxf(bw, s.c1[t] * s.ks[t]);
-                        bt = fmaxf(bt, s.tsum[t]);
-                        bs += s.c3[t] * s.tsum[t];
+                        bw = fmaxf(bw, s.c1[grp][t] * s.ks[t]);
+                        bt = fmaxf(bt, s.tsum[grp][t]);
+                        bs += s.c3[grp][t] * s.tsum[grp][t];
                     }
 #pragma unroll
                     for (int o = 16; o > 0; o >>= 1) {
@@ -427,12 +518,14 @@ __global__ void __launch_bounds__(kPrepThreads) gdn_prep_kernel(const __grid_con
                     }
                     if (lane == 0) {
                         scal[kTS] = pow2(-e);
+                        scal[kPS] = pow2(-ep);
                         scal[kBW] = bw;
                         scal[kBT] = bt;
                         scal[kBS] = bs * 256.f;   // a scaled key's values are below 256
                     }
                 }
             }
+            ptx::named_bar_sync(bar, 128);   // before the next head's A
         }
     }
 }
