@@ -104,9 +104,8 @@ __device__ __forceinline__ int piece_at(int row, int piece) { return row * 128 +
 // launch 1
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
-constexpr int kHeadsAtOnce = 8;    // value heads whose gates are computed together, one per warp
+constexpr int kHeadsAtOnce = 4;    // value heads whose gates are computed together, one per warp
 constexpr int kLd = kC + 4;        // row of a matrix that the tensor cores' fragments are read from
-constexpr int kLdY = 12;
 
 // Two groups of four warps, each with a value head of its own at a time.
 struct __align__(1024) PrepSmem {
@@ -115,7 +114,6 @@ struct __align__(1024) PrepSmem {
         float prod[2][kC][kC];          // then K K^T and Q K^T, 16-byte pieces permuted (prod_at)
     };
     float T[2][kC][kLd];                // A, overwritten by its inverse block by block
-    float Y[2][4][32][kLdY];            // a warp's intermediate products
     float Gh[kHeadsAtOnce][kC], Gl[kHeadsAtOnce][kC];   // sums of g, as the sum of two floats
     float beta[kHeadsAtOnce][kC];
     float rk[kC], rq[kC], ks[kC];       // row factors of K and Q, sums of |K|
@@ -123,6 +121,7 @@ struct __align__(1024) PrepSmem {
     float tsum[2][kC], c1[2][kC], c3[2][kC];
     uint32_t tmax[2];
 };
+static_assert(3 * (sizeof(PrepSmem) + 2048) <= 228 * 1024, "three CTAs an SM");
 
 __device__ __forceinline__ int prod_at(int row, int col) {
     return row * kC + ((((col >> 2) ^ ((row & 7) << 1)) << 2) | (col & 3));
@@ -144,21 +143,36 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// d += A[16 x 8] B[8 x 8], A's rows lda floats apart, B's ldb
-__device__ __forceinline__ void mma_fp32(float (&d)[4], const float* A, int lda, const float* B, int ldb, int lane) {
-    const int r = lane >> 2, c = lane & 3;
-    const Tf a0 = tf_split(A[r * lda + c]), a1 = tf_split(A[(r + 8) * lda + c]);
-    const Tf a2 = tf_split(A[r * lda + c + 4]), a3 = tf_split(A[(r + 8) * lda + c + 4]);
-    const Tf b0 = tf_split(B[c * ldb + r]), b1 = tf_split(B[(c + 4) * ldb + r]);
-    mma_tf32(d, a0.lo, a1.lo, a2.lo, a3.lo, b0.hi, b1.hi);
-    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, b0.lo, b1.lo);
-    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, b0.hi, b1.hi);
+// d += A[16 x 8] B[8 x 8], A's rows kLd floats apart, B as fragment: b0 = B[lane % 4][lane / 4], b1 four rows on
+__device__ __forceinline__ void mma_fp32(float (&d)[4], const float* A, float b0, float b1, int lane) {
+    const float* p = A + (lane >> 2) * kLd + (lane & 3);
+    const Tf a0 = tf_split(p[0]), a1 = tf_split(p[8 * kLd]), a2 = tf_split(p[4]), a3 = tf_split(p[8 * kLd + 4]);
+    const Tf c0 = tf_split(b0), c1 = tf_split(b1);
+    mma_tf32(d, a0.lo, a1.lo, a2.lo, a3.lo, c0.hi, c1.hi);
+    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, c0.lo, c1.lo);
+    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, c0.hi, c1.hi);
+}
+// rows 8 half .. of a 16 x 8 accumulator, as a B fragment
+__device__ __forceinline__ void as_b(const float (&d)[4], int half, int lane, float& b0, float& b1) {
+    const int src = (lane & 3) * 4 + (lane >> 3);   // the lane that holds row lane % 4, column lane / 4
+    const float u0 = __shfl_sync(0xffffffffu, half ? d[2] : d[0], src), u1 = __shfl_sync(0xffffffffu, half ? d[3] : d[1], src);
+    const float v0 = __shfl_sync(0xffffffffu, half ? d[2] : d[0], src + 16), v1 = __shfl_sync(0xffffffffu, half ? d[3] : d[1], src + 16);
+    b0 = (lane >> 2) & 1 ? u1 : u0;
+    b1 = (lane >> 2) & 1 ? v1 : v0;
+}
+// -d to rows lane / 4 and + 8 of T
+__device__ __forceinline__ void put_neg(float* T, const float (&d)[4], int lane) {
+    float* t = T + (lane >> 2) * kLd + 2 * (lane & 3);
+    *reinterpret_cast<float2*>(t) = make_float2(-d[0], -d[1]);
+    *reinterpret_cast<float2*>(t + 8 * kLd) = make_float2(-d[2], -d[3]);
 }
 
 // T = (1 + A)^-1 in place, A strictly lower triangular 64 x 64 (zeros elsewhere); the group's four warps.
 //   Diagonal blocks of 16 by substitution, a lane per column; then pairs of blocks twice over,
 //   T21 = -T22 A21 T11, on the tensor cores: to 32 by a warp each, to 64 by all four, 8 columns each.
-__device__ __forceinline__ void invert(float (*T)[kLd], float (*Y)[32][kLdY], int warp, int lane, int bar) {
+//   The product in between goes from accumulators to operands by shuffles.
+__device__ __forceinline__ void invert(float (*T)[kLd], int warp, int lane, int bar) {
+    const int br = lane & 3, bc = lane >> 2;   // this lane's row and column in a B fragment
     if (warp < 2) {
         const int o = 32 * warp;
         {
@@ -175,75 +189,61 @@ __device__ __forceinline__ void invert(float (*T)[kLd], float (*Y)[32][kLdY], in
             for (int i = 0; i < 16; ++i) T[q + i][q + j] = x[i];
             __syncwarp();
         }
-        float* y = &Y[warp][0][0];   // 16 x 16, rows 20 apart (within the warp's 32 x 12)
-        const int r = lane >> 2, c = 2 * (lane & 3);
-        float d[2][4] = {};
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int ks = nt; ks < 2; ++ks)   // T11's columns 8 nt .. are 0 above row 8 nt
-                mma_fp32(d[nt], &T[o + 16][o + 8 * ks], kLd, &T[o + 8 * ks][o + 8 * nt], kLd, lane);
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-            y[r * 20 + 8 * nt + c] = d[nt][0];
-            y[r * 20 + 8 * nt + c + 1] = d[nt][1];
-            y[(r + 8) * 20 + 8 * nt + c] = d[nt][2];
-            y[(r + 8) * 20 + 8 * nt + c + 1] = d[nt][3];
+            float d[4] = {}, e[4] = {};
+#pragma unroll
+            for (int ks = nt; ks < 2; ++ks) {   // T11's columns 8 nt .. are 0 above row 8 nt
+                const float* t = &T[o + 8 * ks + br][o + 8 * nt + bc];
+                mma_fp32(d, &T[o + 16][o + 8 * ks], t[0], t[4 * kLd], lane);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                float b0, b1;
+                as_b(d, ks, lane, b0, b1);
+                mma_fp32(e, &T[o + 16][o + 16 + 8 * ks], b0, b1, lane);
+            }
+            // columns 8 nt .. of A21 are not needed any more: the other half's products take their own
+            if (nt == 0) __syncwarp();
+            put_neg(nt == 0 ? &T[o][o + 16] : &T[o + 16][o + 8], e, lane);
         }
+        // (the first half waits in the zero block above the diagonal, since the second reads all of A21)
         __syncwarp();
-        float e[2][4] = {};
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks)
-                mma_fp32(e[nt], &T[o + 16][o + 16 + 8 * ks], kLd, y + 8 * ks * 20 + 8 * nt, 20, lane);
-        __syncwarp();
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            float* t = &T[o + 16 + r][o + 8 * nt + c];
-            t[0] = -e[nt][0];
-            t[1] = -e[nt][1];
-            t[8 * kLd] = -e[nt][2];
-            t[8 * kLd + 1] = -e[nt][3];
+        {
+            const int r = lane >> 1, h = (lane & 1) * 4;
+            float4* from = reinterpret_cast<float4*>(&T[o + r][o + 16 + h]);
+            *reinterpret_cast<float4*>(&T[o + 16 + r][o + h]) = *from;
+            *from = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
     ptx::named_bar_sync(bar, 128);
     {
-        const int n0 = 8 * warp, r = lane >> 2, c = 2 * (lane & 3);
-        float d[2][4] = {};
+        const int n0 = 8 * warp;
+        float d[2][4] = {}, e[2][4] = {};
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-            if (ks >= warp)
+            if (ks >= warp) {
+                const float* t = &T[8 * ks + br][n0 + bc];
+                const float b0 = t[0], b1 = t[4 * kLd];
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) mma_fp32(d[mt], &T[32 + 16 * mt][8 * ks], kLd, &T[8 * ks][n0], kLd, lane);
-        float* y = &Y[warp][0][0];
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            y[(16 * mt + r) * kLdY + c] = d[mt][0];
-            y[(16 * mt + r) * kLdY + c + 1] = d[mt][1];
-            y[(16 * mt + r + 8) * kLdY + c] = d[mt][2];
-            y[(16 * mt + r + 8) * kLdY + c + 1] = d[mt][3];
-        }
+                for (int mt = 0; mt < 2; ++mt) mma_fp32(d[mt], &T[32 + 16 * mt][8 * ks], b0, b1, lane);
+            }
         ptx::named_bar_sync(bar, 128);   // A21 has been read
-        float e[2][4] = {};
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+        for (int ks = 0; ks < 4; ++ks) {
+            float b0, b1;
+            as_b(d[ks >> 1], ks & 1, lane, b0, b1);
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
-                if (ks < 2 * mt + 2) mma_fp32(e[mt], &T[32 + 16 * mt][32 + 8 * ks], kLd, y + 8 * ks * kLdY, kLdY, lane);
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
-            float* t = &T[32 + 16 * mt + r][n0 + c];
-            t[0] = -e[mt][0];
-            t[1] = -e[mt][1];
-            t[8 * kLd] = -e[mt][2];
-            t[8 * kLd + 1] = -e[mt][3];
+                if (ks < 2 * mt + 2) mma_fp32(e[mt], &T[32 + 16 * mt][32 + 8 * ks], b0, b1, lane);
         }
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) put_neg(&T[32 + 16 * mt][n0], e[mt], lane);
     }
     ptx::named_bar_sync(bar, 128);
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 2) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
+__global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
     extern __shared__ uint8_t smem_raw[];
     PrepSmem& s = *reinterpret_cast<PrepSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gdn_prep_kernel(const __grid_
 
     // gates of up to 8 value heads from r0, a warp each: two tokens a lane, running sums in FP64
     auto head_gates = [&](int r0) {
-        if (r0 + warp >= R) return;
+        if (warp >= kHeadsAtOnce || r0 + warp >= R) return;
         const int h = kh * R + r0 + warp;
         const float alpha = expf(a.a_log[h]), dt = a.dt_bias[h];
         float g[2], bt[2];
@@ -293,49 +293,61 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gdn_prep_kernel(const __grid_
         }
     };
 
-    // K and Q rows into FP16 images, a half-warp per row, with the row's norm
+    // K and Q rows into FP16 images, eight lanes a row, with the row's norm
     {
-        const int sub = lane >> 4, l16 = lane & 15;
-        uint4 raw[8];
+        const int l8 = lane & 7, row0 = warp * 4 + (lane >> 3);
+        uint4 raw[4][2];
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
-            const int row = (it & 3) * 16 + warp * 2 + sub;
-            raw[it] = make_uint4(0, 0, 0, 0);
-            if (row < valid)
-                raw[it] = *reinterpret_cast<const uint4*>(a.qkv + ((int64_t)b * a.n + t0 + row) * a.C +
-                                                          ((it >> 2) ? kh : a.HK + kh) * kGdnDim + 8 * l16);
+        for (int it = 0; it < 4; ++it) {
+            const int row = (it & 1) * 32 + row0;   // it >> 1: 0 K, 1 Q
+            raw[it][0] = raw[it][1] = make_uint4(0, 0, 0, 0);
+            if (row < valid) {
+                const uint4* p = reinterpret_cast<const uint4*>(a.qkv + ((int64_t)b * a.n + t0 + row) * a.C +
+                                                                ((it >> 1) ? kh : a.HK + kh) * kGdnDim) + l8;
+                raw[it][0] = p[0];
+                raw[it][1] = p[8];
+            }
         }
         head_gates(0);
 #pragma unroll
-        for (int it = 0; it < 8; ++it) {
-            const int m = it >> 2;                                    // 0: K, 1: Q
-            const int row = (it & 3) * 16 + warp * 2 + sub;
-            const float2 p0 = unpack_bf16(raw[it].x), p1 = unpack_bf16(raw[it].y), p2 = unpack_bf16(raw[it].z), p3 = unpack_bf16(raw[it].w);
-            float x[8] = {p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+        for (int it = 0; it < 4; ++it) {
+            const int m = it >> 1, row = (it & 1) * 32 + row0;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 p0 = unpack_bf16(raw[it][i].x), p1 = unpack_bf16(raw[it][i].y);
+                const float2 p2 = unpack_bf16(raw[it][i].z), p3 = unpack_bf16(raw[it][i].w);
+                x[8 * i] = p0.x; x[8 * i + 1] = p0.y; x[8 * i + 2] = p1.x; x[8 * i + 3] = p1.y;
+                x[8 * i + 4] = p2.x; x[8 * i + 5] = p2.y; x[8 * i + 6] = p3.x; x[8 * i + 7] = p3.y;
+            }
             float mx = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(x[i]));
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(x[i]));
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const int e = scale_exponent(mx, 8);
             const float f = pow2(e), inv = pow2(-e);
             float ss = 0.f, sa = 0.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 16; ++i) {
                 x[i] *= f;
                 ss = fmaf(x[i], x[i], ss);
                 sa += fabsf(x[i]);
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
+            for (int o = 4; o > 0; o >>= 1) {
                 ss += __shfl_xor_sync(0xffffffffu, ss, o);
                 sa += __shfl_xor_sync(0xffffffffu, sa, o);
             }
-            const int at = (2 * m + (l16 >> 3)) * kTile + piece_at(row, l16 & 7);
-            const uint4 v = make_uint4(half2_bits(x[0], x[1]), half2_bits(x[2], x[3]), half2_bits(x[4], x[5]), half2_bits(x[6], x[7]));
-            *reinterpret_cast<uint4*>(s.kq + at) = v;
-            *reinterpret_cast<uint4*>(kq_out + at) = v;
-            if (l16 == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int at = (2 * m + i) * kTile + piece_at(row, l8);
+                const uint4 v = make_uint4(half2_bits(x[8 * i], x[8 * i + 1]), half2_bits(x[8 * i + 2], x[8 * i + 3]),
+                                           half2_bits(x[8 * i + 4], x[8 * i + 5]), half2_bits(x[8 * i + 6], x[8 * i + 7]));
+                *reinterpret_cast<uint4*>(s.kq + at) = v;
+                *reinterpret_cast<uint4*>(kq_out + at) = v;
+            }
+            if (l8 == 0) {
                 // 1 / sqrt(sum x^2 + eps) times the row's scale; the sum is of scaled values, so the one
                 // form keeps large rows from overflowing and the other rows far below eps from NaN
                 float r = inv;
@@ -418,42 +430,61 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gdn_prep_kernel(const __grid_
             uint8_t* out = tp_base + (((int64_t)b * a.HV + kh * R + r) * NC + c) * kTPBytes;
             float* scal = reinterpret_cast<float*>(out + kOffScal);
             float (*T)[kLd] = s.T[grp];
-            // A (strictly below the diagonal) and P, eight columns of a row at a time
+            // A (strictly below the diagonal) and P, eight columns of a row at a time.  Below the diagonal's
+            // pieces e^{G_i - G_j} is the product of e^{G_i - G_r} and e^{G_r - G_j}, r the piece's last column:
+            // j <= r < i, so neither exceeds 1.
             const int p = gt & 7;
-            float Gjh[8], Gjl[8], rkj[8];
+            const float *k_k = &s.prod[0][0][0], *q_k = &s.prod[1][0][0];
+            {
+                const float rh = Gh[8 * p + 7], rl = Gl[8 * p + 7];
+                float cf[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                Gjh[x] = Gh[8 * p + x];
-                Gjl[x] = Gl[8 * p + x];
-                rkj[x] = s.rk[8 * p + x];
-            }
+                for (int x = 0; x < 8; ++x)
+                    cf[x] = s.rk[8 * p + x] * __expf((rh - Gh[8 * p + x]) + (rl - Gl[8 * p + x]));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int i = (gt >> 3) + 16 * k;
-                float A[8], P[8];
-                if (8 * p <= i) {
-                    const float4 k0 = *reinterpret_cast<const float4*>(&s.prod[0][0][0] + prod_at(i, 8 * p));
-                    const float4 k1 = *reinterpret_cast<const float4*>(&s.prod[0][0][0] + prod_at(i, 8 * p + 4));
-                    const float4 q0 = *reinterpret_cast<const float4*>(&s.prod[1][0][0] + prod_at(i, 8 * p));
-                    const float4 q1 = *reinterpret_cast<const float4*>(&s.prod[1][0][0] + prod_at(i, 8 * p + 4));
-                    const float kk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
-                    const float qk[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-                    const float gh = Gh[i], gl = Gl[i], fa = beta[i] * s.rk[i], fp = s.rq[i] * p_scale;
+                for (int k = 0; k < 4; ++k) {
+                    const int i = (gt >> 3) + 16 * k;
+                    if ((i >> 3) == p) continue;   // the diagonal's
+                    float A[8], P[8];
+                    if (p < (i >> 3)) {
+                        const float ei = __expf((Gh[i] - rh) + (Gl[i] - rl));
+                        const float fa = beta[i] * s.rk[i] * ei, fp = s.rq[i] * p_scale * ei;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        const int j = 8 * p + x;
-                        const float d = rkj[x] * __expf((gh - Gjh[x]) + (gl - Gjl[x]));
-                        A[x] = j < i ? fa * d * kk[x] : 0.f;
-                        P[x] = j <= i ? fp * d * qk[x] : 0.f;
+                        for (int y = 0; y < 2; ++y) {
+                            const float4 kk = *reinterpret_cast<const float4*>(k_k + prod_at(i, 8 * p + 4 * y));
+                            const float4 qk = *reinterpret_cast<const float4*>(q_k + prod_at(i, 8 * p + 4 * y));
+                            A[4 * y] = fa * cf[4 * y] * kk.x; A[4 * y + 1] = fa * cf[4 * y + 1] * kk.y;
+                            A[4 * y + 2] = fa * cf[4 * y + 2] * kk.z; A[4 * y + 3] = fa * cf[4 * y + 3] * kk.w;
+                            P[4 * y] = fp * cf[4 * y] * qk.x; P[4 * y + 1] = fp * cf[4 * y + 1] * qk.y;
+                            P[4 * y + 2] = fp * cf[4 * y + 2] * qk.z; P[4 * y + 3] = fp * cf[4 * y + 3] * qk.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) A[x] = P[x] = 0.f;
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) A[x] = P[x] = 0.f;
+                    *reinterpret_cast<float4*>(&T[i][8 * p]) = make_float4(A[0], A[1], A[2], A[3]);
+                    *reinterpret_cast<float4*>(&T[i][8 * p + 4]) = make_float4(A[4], A[5], A[6], A[7]);
+                    *reinterpret_cast<uint4*>(out + kOffP + piece_at(i, p)) =
+                        make_uint4(half2_bits(P[0], P[1]), half2_bits(P[2], P[3]), half2_bits(P[4], P[5]), half2_bits(P[6], P[7]));
                 }
-                *reinterpret_cast<float4*>(&T[i][8 * p]) = make_float4(A[0], A[1], A[2], A[3]);
-                *reinterpret_cast<float4*>(&T[i][8 * p + 4]) = make_float4(A[4], A[5], A[6], A[7]);
-                *reinterpret_cast<uint4*>(out + kOffP + piece_at(i, p)) =
-                    make_uint4(half2_bits(P[0], P[1]), half2_bits(P[2], P[3]), half2_bits(P[4], P[5]), half2_bits(P[6], P[7]));
+            }
+            {
+                const int i = gt >> 1, j0 = (i & ~7) + 4 * (gt & 1);   // half a piece of the diagonal
+                const float4 kk4 = *reinterpret_cast<const float4*>(k_k + prod_at(i, j0));
+                const float4 qk4 = *reinterpret_cast<const float4*>(q_k + prod_at(i, j0));
+                const float kk[4] = {kk4.x, kk4.y, kk4.z, kk4.w}, qk[4] = {qk4.x, qk4.y, qk4.z, qk4.w};
+                const float gh = Gh[i], gl = Gl[i], fa = beta[i] * s.rk[i], fp = s.rq[i] * p_scale;
+                float A[4], P[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = j0 + x;
+                    const float d = s.rk[j] * __expf((gh - Gh[j]) + (gl - Gl[j]));
+                    A[x] = j < i ? fa * d * kk[x] : 0.f;
+                    P[x] = j <= i ? fp * d * qk[x] : 0.f;
+                }
+                *reinterpret_cast<float4*>(&T[i][j0]) = make_float4(A[0], A[1], A[2], A[3]);
+                *reinterpret_cast<uint2*>(out + kOffP + piece_at(i, i >> 3) + 8 * (gt & 1)) =
+                    make_uint2(half2_bits(P[0], P[1]), half2_bits(P[2], P[3]));
             }
             if (gt < kC) {
                 const float since = __expf(Gh[gt] + Gl[gt]);
@@ -465,7 +496,7 @@ __global__ void __launch_bounds__(kPrepThreads, 2) gdn_prep_kernel(const __grid_
             }
             if (gt == 0) s.tmax[grp] = 0u;
             ptx::named_bar_sync(bar, 128);
-            invert(T, s.Y[grp], gw, lane, bar);
+            invert(T, gw, lane, bar);
             // T with beta's columns: its largest value, its rows' sums; scaled, split, to the workspace
             {
                 float v[4][8], mx = 0.f;
