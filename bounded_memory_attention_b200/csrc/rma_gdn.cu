@@ -9,13 +9,16 @@ namespace {
 //
 // Memory bound: 2 bytes read and 2 written per (token, channel), the state's 12 bytes per channel
 // and sequence.  A thread keeps 8 channels' weights in registers (16-byte loads and stores of the
-// activations) and walks down a tile of tokens with the last three rows in registers, so a row is
-// read once per tile plus three rows of overlap; single tokens walk over sequences instead, so
-// that the weights (16 bytes a channel, more than the activations) are fetched once per several.
-// The state is read by the first tile only and written by the same threads, after their reads.
+// activations).  Blocks of tokens: it walks down a tile with the last three rows in registers, the next
+// eight rows always on their way, so a row is read once per tile plus three rows of overlap.  Single
+// tokens: it walks over sequences instead, so that the weights (16 bytes a channel, more than the
+// activations) are fetched once per several, two sequences' loads in flight.  The state is read by the
+// first tile only and written by the same threads, after their reads.
 // ---------------------------------------------------------------------------
 constexpr int kConvThreads = 128;
 constexpr int kConvVec = 8;
+constexpr int kConvTile = 64;     // tokens of a tile
+constexpr int kConvRows = 8;      // rows on their way
 
 __device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
     const float2 p0 = unpack_bf16(r.x), p1 = unpack_bf16(r.y), p2 = unpack_bf16(r.z), p3 = unpack_bf16(r.w);
@@ -26,72 +29,133 @@ __device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
 // z / (1 + exp(-z)); exp overflows to infinity below -88, where the quotient is -0
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 
-__global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_constant__ ConvArgs a, int tile, int tiles,
-                                                                int seqs, int cblocks) {
+struct ConvWeights {
+    float w[8][4], bias[8];
+    __device__ __forceinline__ void load(const ConvArgs& a, int c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(a.w) + c + i);
+            w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
+            bias[i] = 0.f;
+        }
+        if (a.bias) {
+            const float4 u = __ldg(reinterpret_cast<const float4*>(a.bias + c)), v = __ldg(reinterpret_cast<const float4*>(a.bias + c) + 1);
+            bias[0] = u.x; bias[1] = u.y; bias[2] = u.z; bias[3] = u.w;
+            bias[4] = v.x; bias[5] = v.y; bias[6] = v.z; bias[7] = v.w;
+        }
+    }
+    __device__ __forceinline__ uint4 out(const float (&p0)[8], const float (&p1)[8], const float (&p2)[8], const float (&p3)[8]) const {
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float z = fmaf(w[i][0], p0[i], bias[i]);
+            z = fmaf(w[i][1], p1[i], z);
+            z = fmaf(w[i][2], p2[i], z);
+            y[i] = silu(fmaf(w[i][3], p3[i], z));
+        }
+        return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+    }
+};
+
+__global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_constant__ ConvArgs a, int tiles, int cblocks) {
     grid_dep_wait();
     grid_dep_launch();
     const int cb = blockIdx.x % cblocks;
     const int tl = (blockIdx.x / cblocks) % tiles;
-    const int b0 = (blockIdx.x / cblocks / tiles) * seqs;
+    const int b = blockIdx.x / cblocks / tiles;
     const int c = (cb * kConvThreads + threadIdx.x) * kConvVec;
     if (c >= a.C) return;
-    const int t0 = tl * tile;
-    float w[8][4], bias[8];
+    const int t0 = tl * kConvTile;
+    const int len = seq_len(a.lens, b, a.n, a.status, tl == 0 && cb == 0 && threadIdx.x == 0);
+    if (t0 >= len) return;
+    const uint16_t* x = a.x + (int64_t)b * a.n * a.x_stride + c;
+    uint16_t* st = a.state + (int64_t)b * 3 * a.C + c;
+    uint16_t* out = a.out + (int64_t)b * a.n * a.C + c;
+    auto row = [&](int t) { return *reinterpret_cast<const uint4*>(x + (int64_t)t * a.x_stride); };
+    const int end = min(t0 + kConvTile, len);
+    uint4 next[kConvRows], h[3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(a.w) + c + i);
-        w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
-        bias[i] = 0.f;
-    }
-    if (a.bias) {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(a.bias + c)), v = __ldg(reinterpret_cast<const float4*>(a.bias + c) + 1);
-        bias[0] = u.x; bias[1] = u.y; bias[2] = u.z; bias[3] = u.w;
-        bias[4] = v.x; bias[5] = v.y; bias[6] = v.z; bias[7] = v.w;
-    }
-    for (int b = b0; b < min(b0 + seqs, a.B); ++b) {
-        const int len = seq_len(a.lens, b, a.n, a.status, tl == 0 && cb == 0 && threadIdx.x == 0);
-        if (t0 >= len) continue;
-        const uint16_t* x = a.x + (int64_t)b * a.n * a.x_stride + c;
-        uint16_t* st = a.state + (int64_t)b * 3 * a.C + c;
-        uint16_t* out = a.out + (int64_t)b * a.n * a.C + c;
-        auto row = [&](int t) { return *reinterpret_cast<const uint4*>(x + (int64_t)t * a.x_stride); };
-        uint4 h[3];
-        if (t0 == 0) {
+    for (int i = 0; i < kConvRows; ++i)
+        if (t0 + i < end) next[i] = row(t0 + i);
+    ConvWeights w;
+    w.load(a, c);
+    if (t0 == 0) {
 #pragma unroll
-            for (int j = 0; j < 3; ++j) h[j] = *reinterpret_cast<const uint4*>(st + (int64_t)j * a.C);
-            // the last three rows of (state, x): row len + j of the two in sequence
+        for (int j = 0; j < 3; ++j) h[j] = *reinterpret_cast<const uint4*>(st + (int64_t)j * a.C);
+        // the last three rows of (state, x): row len + j of the two in sequence
 #pragma unroll
-            for (int j = 0; j < 3; ++j) {
-                const int i = len + j;
-                const uint4 v = i >= 3 ? row(i - 3) : (i == 1 ? h[1] : h[2]);
-                *reinterpret_cast<uint4*>(st + (int64_t)j * a.C) = v;
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 3; ++j) h[j] = row(t0 - 3 + j);   // tile >= 3: never before row 0
+        for (int j = 0; j < 3; ++j) {
+            const int i = len + j;
+            const uint4 v = i >= 3 ? row(i - 3) : (i == 1 ? h[1] : h[2]);
+            *reinterpret_cast<uint4*>(st + (int64_t)j * a.C) = v;
         }
-        float p0[8], p1[8], p2[8];
-        unpack8(h[0], p0);
-        unpack8(h[1], p1);
-        unpack8(h[2], p2);
-        const int end = min(t0 + tile, len);
-#pragma unroll 4
-        for (int t = t0; t < end; ++t) {
-            float p3[8], y[8];
-            unpack8(row(t), p3);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float z = fmaf(w[i][0], p0[i], bias[i]);
-                z = fmaf(w[i][1], p1[i], z);
-                z = fmaf(w[i][2], p2[i], z);
-                z = fmaf(w[i][3], p3[i], z);
-                y[i] = silu(z);
-                p0[i] = p1[i];
-                p1[i] = p2[i];
-                p2[i] = p3[i];
+        for (int j = 0; j < 3; ++j) h[j] = row(t0 - 3 + j);
+    }
+    float p0[8], p1[8], p2[8];
+    unpack8(h[0], p0);
+    unpack8(h[1], p1);
+    unpack8(h[2], p2);
+    for (int t = t0; t < end; t += kConvRows) {
+        uint4 cur[kConvRows];
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) cur[i] = next[i];
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i)
+            if (t + kConvRows + i < end) next[i] = row(t + kConvRows + i);
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) {
+            if (t + i < end) {
+                float p3[8];
+                unpack8(cur[i], p3);
+                *reinterpret_cast<uint4*>(out + (int64_t)(t + i) * a.C) = w.out(p0, p1, p2, p3);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    p0[k] = p1[k];
+                    p1[k] = p2[k];
+                    p2[k] = p3[k];
+                }
             }
-            *reinterpret_cast<uint4*>(out + (int64_t)t * a.C) =
-                make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        }
+    }
+}
+
+// n == 1: `seqs` sequences a thread, two at a time
+__global__ void __launch_bounds__(kConvThreads) gdn_conv_token_kernel(const __grid_constant__ ConvArgs a, int seqs, int cblocks) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int cb = blockIdx.x % cblocks;
+    const int b0 = (blockIdx.x / cblocks) * seqs, b1 = min(b0 + seqs, a.B);
+    const int c = (cb * kConvThreads + threadIdx.x) * kConvVec;
+    if (c >= a.C) return;
+    ConvWeights w;
+    w.load(a, c);
+    for (int b = b0; b < b1; b += 2) {
+        uint4 x[2], h[2][3];
+        bool on[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            on[i] = b + i < b1 && seq_len(a.lens, b + i, 1, a.status, cb == 0 && threadIdx.x == 0) > 0;
+            if (on[i]) {
+                x[i] = *reinterpret_cast<const uint4*>(a.x + (int64_t)(b + i) * a.x_stride + c);
+#pragma unroll
+                for (int j = 0; j < 3; ++j) h[i][j] = *reinterpret_cast<const uint4*>(a.state + ((int64_t)(b + i) * 3 + j) * a.C + c);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!on[i]) continue;
+            uint16_t* st = a.state + (int64_t)(b + i) * 3 * a.C + c;
+            *reinterpret_cast<uint4*>(st) = h[i][1];
+            *reinterpret_cast<uint4*>(st + a.C) = h[i][2];
+            *reinterpret_cast<uint4*>(st + 2 * (int64_t)a.C) = x[i];
+            float p0[8], p1[8], p2[8], p3[8];
+            unpack8(h[i][0], p0);
+            unpack8(h[i][1], p1);
+            unpack8(h[i][2], p2);
+            unpack8(x[i], p3);
+            *reinterpret_cast<uint4*>(a.out + (int64_t)(b + i) * a.C + c) = w.out(p0, p1, p2, p3);
         }
     }
 }
@@ -213,13 +277,18 @@ __global__ void __launch_bounds__(kRecThreads) gdn_recurrent_kernel(const __grid
 
 cudaError_t launch_gdn_conv(const ConvArgs& a, cudaStream_t stream) {
     const int cblocks = (a.C / kConvVec + kConvThreads - 1) / kConvThreads;
-    const int tile = a.n == 1 ? 3 : 32;
-    const int tiles = (a.n + tile - 1) / tile;
-    const int seqs = a.n == 1 ? (a.B >= 256 ? 4 : 1) : 1;
-    const int64_t grid = (int64_t)cblocks * tiles * ((a.B + seqs - 1) / seqs);
+    if (a.n == 1) {
+        const int seqs = a.B >= 256 ? 4 : (a.B >= 64 ? 2 : 1);
+        const int64_t grid = (int64_t)cblocks * ((a.B + seqs - 1) / seqs);
+        if (grid > 0x7fffffffll) return cudaErrorNotSupported;
+        PdlLaunch l((unsigned)grid, kConvThreads, 0, stream);
+        return cudaLaunchKernelEx(&l.cfg, gdn_conv_token_kernel, a, seqs, cblocks);
+    }
+    const int tiles = (a.n + kConvTile - 1) / kConvTile;
+    const int64_t grid = (int64_t)cblocks * tiles * a.B;
     if (grid > 0x7fffffffll) return cudaErrorNotSupported;
     PdlLaunch l((unsigned)grid, kConvThreads, 0, stream);
-    return cudaLaunchKernelEx(&l.cfg, gdn_conv_kernel, a, tile, tiles, seqs, cblocks);
+    return cudaLaunchKernelEx(&l.cfg, gdn_conv_kernel, a, tiles, cblocks);
 }
 
 cudaError_t launch_gdn_recurrent(const DeltaArgs& a, cudaStream_t stream) {

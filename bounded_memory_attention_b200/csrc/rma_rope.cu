@@ -3,12 +3,12 @@
 //   y = x / sqrt(mean(x^2) + eps) * w;  for the rotated pairs (u, v) of a head:
 //   (y_u c - y_v s, y_v c + y_u s),  c, s = cos, sin of position * inv_freq[i].
 //
-// Memory bound: every value is read once and written once, 4 bytes in all.  A CTA is one token of
-// one KV group: its 4 query heads and its key, a warp each, 8 values (16 bytes) a lane; the sum of
-// squares is one warp reduction.  The group's angles are computed once per CTA, a thread each,
-// while the warps' loads are in flight.  A product of a far position and a frequency has an
-// absolute error of half an ulp of the angle, 0.008 rad at 2^18 in FP32, so the product and its
-// reduction to a fraction of a turn are in FP64; the fraction's sine and cosine then need FP32
+// Memory bound: every value is read once and written once, 4 bytes in all.  A CTA takes one KV group's 4
+// query heads and its key, a warp each, 8 values (16 bytes) a lane, of one or several consecutive tokens:
+// all loads are issued first, then the angles of the group's tokens are computed, a thread each, while
+// they are in flight; the sum of squares is one warp reduction.  A product of a far position and a
+// frequency has an absolute error of half an ulp of the angle, 0.008 rad at 2^18 in FP32, so the product
+// and its reduction to a fraction of a turn are in FP64; the fraction's sine and cosine then need FP32
 // only.  Pairs that lie in two lanes meet in the warp's row of shared memory.
 #include <cuda_bf16.h>
 
@@ -32,90 +32,119 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+template <int T>   // tokens of a CTA
 __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ float cs[kHeadDim / 2], sn[kHeadDim / 2];
+    __shared__ __align__(16) float cs[T][kHeadDim / 2], sn[T][kHeadDim / 2];
     __shared__ __align__(16) float rows[kHeads][kHeadDim];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = blockIdx.x % a.G;
-    const int64_t tok = blockIdx.x / a.G;   // b n + i
+    const int64_t tok0 = (int64_t)(blockIdx.x / a.G) * T;   // of b n + i
+    const int count = (int)min((int64_t)T, (int64_t)a.B * a.n - tok0);
     grid_dep_wait();
     grid_dep_launch();
 
     const bool is_k = warp == kQPerGroup;
-    const uint16_t* src = is_k ? a.k + tok * a.k_stride + (int64_t)g * kHeadDim
-                               : a.q + tok * a.q_stride + (int64_t)(g * kQPerGroup + warp) * kHeadDim;
-    const uint4 raw = reinterpret_cast<const uint4*>(src)[lane];
+    const int64_t stride = is_k ? a.k_stride : a.q_stride;
+    const uint16_t* src = (is_k ? a.k + (int64_t)g * kHeadDim : a.q + (int64_t)(g * kQPerGroup + warp) * kHeadDim) + tok0 * stride;
+    uint4 raw[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+        if (t < count) raw[t] = reinterpret_cast<const uint4*>(src + t * stride)[lane];
     const float4* w4 = reinterpret_cast<const float4*>(is_k ? a.w_k : a.w_q) + 2 * lane;
     const float4 wa = __ldg(w4), wb = __ldg(w4 + 1);
+    const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 
-    if (a.half > 0) {
+    const int half = a.half;
+    for (int i = threadIdx.x; i < half * count; i += kRopeThreads) {
+        const int t = T == 1 ? 0 : i / half, f = T == 1 ? i : i - t * half;
+        const int64_t tok = tok0 + t;
         int64_t pos;
         if (a.positions) {
             pos = a.positions[tok];
         } else {
             const int64_t b = tok / a.n;
             const int c = a.counters[(b * a.G + g) * 4];
-            if (c < 0 && threadIdx.x == 0) atomicOr(a.status, (unsigned)RMA_STATUS_BAD_COUNTERS);
+            if (c < 0 && f == 0) atomicOr(a.status, (unsigned)RMA_STATUS_BAD_COUNTERS);
             pos = (int64_t)max(c, 0) + (tok - b * a.n);
         }
-        for (int i = threadIdx.x; i < a.half; i += kRopeThreads) {
-            const double turns = (double)pos * (a.inv_freq[i] * 0.15915494309189533577);   // 1 / (2 pi)
-            const float f = (float)(turns - rint(turns));
-            sincospif(2.f * f, &sn[i], &cs[i]);
+        const double turns = (double)pos * (a.inv_freq[f] * 0.15915494309189533577);   // 1 / (2 pi)
+        sincospif(2.f * (float)(turns - rint(turns)), &sn[t][f], &cs[t][f]);
+    }
+    __syncthreads();
+
+    const int64_t dst_stride = (int64_t)a.G * kHeadDim * (is_k ? 1 : kQPerGroup);
+    uint16_t* dst = (is_k ? a.k_out + (int64_t)g * kHeadDim : a.q_out + (int64_t)(g * kQPerGroup + warp) * kHeadDim) + tok0 * dst_stride;
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        if (t >= count) break;
+        float x[8];
+        {
+            const float2 p0 = unpack(raw[t].x), p1 = unpack(raw[t].y), p2 = unpack(raw[t].z), p3 = unpack(raw[t].w);
+            x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
+            x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
         }
-    }
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = 1.f / sqrtf(ss * (1.f / kHeadDim) + a.eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
 
-    float x[8];
-    {
-        const float2 p0 = unpack(raw.x), p1 = unpack(raw.y), p2 = unpack(raw.z), p3 = unpack(raw.w);
-        x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
-        x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
-    }
-    float ss = 0.f;
+        const int d0 = 8 * lane;
+        if (a.interleaved) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < 4; ++i) {
+                const int p = 4 * lane + i;
+                if (p < half) {
+                    const float u = x[2 * i], v = x[2 * i + 1], c = cs[t][p], s = sn[t][p];
+                    x[2 * i] = u * c - v * s;
+                    x[2 * i + 1] = v * c + u * s;
+                }
+            }
+        } else if (half > 0) {
+            float4* row = reinterpret_cast<float4*>(rows[warp]) + 2 * lane;
+            __syncwarp();   // the token before has been read
+            row[0] = make_float4(x[0], x[1], x[2], x[3]);
+            row[1] = make_float4(x[4], x[5], x[6], x[7]);
+            __syncwarp();
+            if ((half & 7) == 0) {   // a lane's values have one side each, and their partners are eight in a row
+                if (d0 < 2 * half) {
+                    const bool first = d0 < half;
+                    const int p = first ? d0 : d0 - half;
+                    const float4* other = reinterpret_cast<const float4*>(rows[warp] + (first ? d0 + half : p));
+                    const float4 o0 = other[0], o1 = other[1];
+                    const float4 c0 = *reinterpret_cast<const float4*>(&cs[t][p]), c1 = *reinterpret_cast<const float4*>(&cs[t][p + 4]);
+                    const float4 s0 = *reinterpret_cast<const float4*>(&sn[t][p]), s1 = *reinterpret_cast<const float4*>(&sn[t][p + 4]);
+                    const float y[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+                    const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+                    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = 1.f / sqrtf(ss * (1.f / kHeadDim) + a.eps);
-    const float w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                    for (int i = 0; i < 8; ++i) x[i] = first ? x[i] * c[i] - y[i] * s[i] : x[i] * c[i] + y[i] * s[i];
+                }
+            } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
-    __syncthreads();   // the angles
-
-    const int half = a.half, d0 = 8 * lane;
-    if (a.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = 4 * lane + i;
-            if (p < half) {
-                const float u = x[2 * i], v = x[2 * i + 1], c = cs[p], s = sn[p];
-                x[2 * i] = u * c - v * s;
-                x[2 * i + 1] = v * c + u * s;
+                for (int i = 0; i < 8; ++i) {
+                    const int d = d0 + i;
+                    if (d < half) x[i] = x[i] * cs[t][d] - rows[warp][d + half] * sn[t][d];
+                    else if (d < 2 * half) x[i] = x[i] * cs[t][d - half] + rows[warp][d - half] * sn[t][d - half];
+                }
             }
         }
-    } else {
-        float4* row = reinterpret_cast<float4*>(rows[warp]) + 2 * lane;
-        row[0] = make_float4(x[0], x[1], x[2], x[3]);
-        row[1] = make_float4(x[4], x[5], x[6], x[7]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int d = d0 + i;
-            if (d < half) x[i] = x[i] * cs[d] - rows[warp][d + half] * sn[d];
-            else if (d < 2 * half) x[i] = x[i] * cs[d - half] + rows[warp][d - half] * sn[d - half];
-        }
+        reinterpret_cast<uint4*>(dst + t * dst_stride)[lane] =
+            make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
     }
-    uint16_t* dst = is_k ? a.k_out + (tok * a.G + g) * kHeadDim
-                         : a.q_out + (tok * a.G * kQPerGroup + g * kQPerGroup + warp) * kHeadDim;
-    reinterpret_cast<uint4*>(dst)[lane] =
-        make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
+    // Few tokens: one a CTA, as many CTAs as there can be.  Many: four, whose loads are all in flight at once.
+    const int64_t tokens = (int64_t)a.B * a.n;
+    const bool many = tokens * a.G >= 4096;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.B * a.n * a.G), 1, 1);
+    cfg.gridDim = dim3((unsigned)((many ? (tokens + 3) / 4 : tokens) * a.G), 1, 1);
     cfg.blockDim = dim3(kRopeThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -123,7 +152,7 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel, a);
+    return many ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<4>, a) : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<1>, a);
 }
 
 }  // namespace rma

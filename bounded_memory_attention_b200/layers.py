@@ -18,25 +18,32 @@ from . import RmaError, _check, _GdnConfig, _GdnLayout, lib  # noqa: F401
 
 _BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
 _HERE = contextlib.nullcontext()
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(device: torch.device):
-    """A context in which `device` is the current one."""
-    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _on(index: int):
+    """A context in which device `index` is the current one."""
+    return _HERE if _current_device() == index else torch.cuda.device(index)
 
 
-def _stream(stream, device: torch.device) -> int:
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _stream(stream, index: int) -> int:
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
-def _dense(t, dtype, numel: int, name: str, device) -> int:
-    """The address of a contiguous tensor."""
+def _tensor(t, dtype, name: str, index: int) -> None:
+    """`t` is a tensor of `dtype` on CUDA device `index`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the state on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the state on device {index}")
+
+
+def _dense(t, dtype, numel: int, name: str, index: int) -> int:
+    """The address of a contiguous tensor."""
+    _tensor(t, dtype, name, index)
     if t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
     if not t.is_contiguous():
@@ -44,16 +51,11 @@ def _dense(t, dtype, numel: int, name: str, device) -> int:
     return t.data_ptr()
 
 
-def _rows(t, dtype, batch: int, n: int, inner: tuple, name: str, device):
+def _rows(t, dtype, batch: int, n: int, inner: tuple, name: str, index: int):
     """(address, elements from one token to the next) of a [batch, n, *inner] tensor (or
     [batch, *inner] for n == 1) whose tokens are contiguous rows, evenly spaced over the batch too."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the state on {device}")
-    shape, strides = tuple(t.shape), t.stride()
+    _tensor(t, dtype, name, index)
+    shape, strides = t.shape, t.stride()
     if n == 1 and shape == (batch, *inner):
         shape, strides = (batch, 1, *inner), (strides[0], strides[0], *strides[1:])
     if shape != (batch, n, *inner):
@@ -92,7 +94,7 @@ def qk_norm_rope(state, layer: int, q, k, w_q, w_k, inv_freq, q_out, k_out, posi
     wider rows; w_q, w_k [256] f32; inv_freq [pairs] f64 (None: no rotation); positions [B, n] i32, or None
     for the places that the layer's counters give the next tokens."""
     c = state.cfg
-    device = state.buffer.device
+    device = state.buffer.get_device()
     B, G, HQ, D = c.batch, c.n_groups, c.n_q_heads, c.head_dim
     n = _tokens(q, B, 4, "q")
     qp, qs = _rows(q, _BF16, B, n, (HQ, D), "q", device)
@@ -162,7 +164,7 @@ class GdnState:
             self.buffer = raw[off:off + n]
         c = cfg._c()
         lay = _GdnLayout()
-        device = self.buffer.device
+        device = self.buffer.get_device()
         with _on(device):
             _check(lib.rma_gdn_state_alloc(ctypes.byref(c), self.buffer.data_ptr(), n, _stream(stream, device),
                                            ctypes.byref(self._h)), "rma_gdn_state_alloc")
@@ -216,7 +218,7 @@ def gdn_conv(state: GdnState, layer: int, x, w, out, bias=None, lens=None, strea
     """rma_gdn_conv: the short convolution with SiLU over x [B, n, C] ([B, C] for one token; may be a view of
     wider rows), w [C, 4] f32, bias [C] f32 or None, lens [B] i32 or None; returns ``out``."""
     c = state.cfg
-    device = state.buffer.device
+    device = state.buffer.get_device()
     B, C = c.batch, c.channels
     n = _tokens(x, B, 3, "x")
     xp, xs = _rows(x, _BF16, B, n, (C,), "x", device)
@@ -241,7 +243,7 @@ def gdn_decode_step(state: GdnState, layer: int, qkv, a, b, a_log, dt_bias, out,
     """rma_gdn_decode_step: one token of the gated delta rule; qkv [B, C] as gdn_conv writes it, a and b [B, HV]
     (may be views of wider rows), a_log and dt_bias [HV] f32, out [B, HV, 128]; returns ``out``."""
     c = state.cfg
-    device = state.buffer.device
+    device = state.buffer.get_device()
     B, HV = c.batch, c.n_v_heads
     ap, bp, stride = _gate_rows(a, b, B, 1, HV, device)
     args = (_dense(qkv, _BF16, B * c.channels, "qkv", device), ap, bp, stride,
@@ -257,7 +259,7 @@ def gdn_prefill(state: GdnState, layer: int, qkv, a, b, a_log, dt_bias, out, ws,
     """rma_gdn_prefill: the gated delta rule over qkv [B, n, C], a and b [B, n, HV], out [B, n, HV, 128]; `ws`
     from state.workspace(n); lens [B] i32 or None; returns ``out``."""
     c = state.cfg
-    device = state.buffer.device
+    device = state.buffer.get_device()
     B, HV = c.batch, c.n_v_heads
     n = _tokens(qkv, B, 3, "qkv")
     ap, bp, stride = _gate_rows(a, b, B, n, HV, device)
@@ -273,7 +275,7 @@ def gdn_prefill(state: GdnState, layer: int, qkv, a, b, a_log, dt_bias, out, ws,
 def gdn_get_status(state: GdnState, stream=None) -> int:
     """Wait for the stream, then read and clear the GDN state's status word (STATUS_* bits)."""
     flags = ctypes.c_uint32()
-    device = state.buffer.device
+    device = state.buffer.get_device()
     with _on(device):
         _check(lib.rma_gdn_get_status(state.handle, _stream(stream, device), ctypes.byref(flags)),
                "rma_gdn_get_status")

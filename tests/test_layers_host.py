@@ -74,7 +74,7 @@ def test_token_strides_of_views():
 
     def rows(t, batch, n, inner):
         t = t.as_subclass(OnDevice)
-        return layers._rows(t, torch.bfloat16, batch, n, inner, "x", t.device)[1]
+        return layers._rows(t, torch.bfloat16, batch, n, inner, "x", t.get_device())[1]
 
     wide = torch.zeros(2, 3, 640, dtype=torch.bfloat16)
     assert rows(wide[..., :512].view(2, 3, 2, 256), 2, 3, (2, 256)) == 640
@@ -91,6 +91,6 @@ def test_token_strides_of_views():
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(TypeError):
-        layers._rows(wide, torch.bfloat16, 2, 3, (640,), "x", wide.device)
+        layers._rows(wide, torch.bfloat16, 2, 3, (640,), "x", -1)
     with pytest.raises(TypeError):
         rows(wide.float(), 2, 3, (640,))
