@@ -8,62 +8,96 @@ namespace {
 // rma_gdn_conv: z[t] = bias + sum_j w[j] x[t - 3 + j], out = silu(z), and the three-row state.
 //
 // Memory bound: 2 bytes read and 2 written per (token, channel), the state's 12 bytes per channel
-// and sequence.  A thread keeps 8 channels' weights in registers (16-byte loads and stores of the
-// activations).  Blocks of tokens: it walks down a tile with the last three rows in registers, the next
-// eight rows always on their way, so a row is read once per tile plus three rows of overlap.  Single
+// and sequence.  A thread keeps 4 or 8 channels' weights in registers.  Blocks of tokens: it walks down a tile with the last three rows in registers, the next
+// four rows always on their way, so a row is read once per tile plus three rows of overlap.  Single
 // tokens: it walks over sequences instead, so that the weights (16 bytes a channel, more than the
 // activations) are fetched once per several, two sequences' loads in flight.  The state is read by the
 // first tile only and written by the same threads, after their reads.
 // ---------------------------------------------------------------------------
 constexpr int kConvThreads = 128;
-constexpr int kConvVec = 8;
-constexpr int kConvTile = 64;     // tokens of a tile
-constexpr int kConvRows = 8;      // rows on their way
+constexpr int kConvTile = 32;     // tokens of a tile
+constexpr int kConvRows = 4;      // rows on their way
 
-__device__ __forceinline__ void unpack8(const uint4& r, float (&x)[8]) {
-    const float2 p0 = unpack_bf16(r.x), p1 = unpack_bf16(r.y), p2 = unpack_bf16(r.z), p3 = unpack_bf16(r.w);
-    x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
-    x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
+// z / (1 + exp(-z)).  The approximate forms that flush denormals are two instructions of the slow pipe and no
+// more; exp(-z) is infinite below z = -88, where the quotient is -0, and its flush to 0 above 87 changes nothing.
+__device__ __forceinline__ float silu(float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + e));
+    return z * r;
 }
 
-// z / (1 + exp(-z)); exp overflows to infinity below -88, where the quotient is -0
-__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+// V channels of a row: 4 (8 bytes) or 8 (16 bytes)
+template <int V>
+struct ConvRow {
+    uint32_t r[V / 2];
+    __device__ __forceinline__ static ConvRow load(const uint16_t* p) {
+        ConvRow x;
+        if constexpr (V == 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            x.r[0] = v.x; x.r[1] = v.y; x.r[2] = v.z; x.r[3] = v.w;
+        } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            x.r[0] = v.x; x.r[1] = v.y;
+        }
+        return x;
+    }
+    __device__ __forceinline__ void store(uint16_t* p) const {
+        if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+        else *reinterpret_cast<uint2*>(p) = make_uint2(r[0], r[1]);
+    }
+    __device__ __forceinline__ void floats(float (&x)[V]) const {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 v = unpack_bf16(r[i]);
+            x[2 * i] = v.x;
+            x[2 * i + 1] = v.y;
+        }
+    }
+};
 
+template <int V>
 struct ConvWeights {
-    float w[8][4], bias[8];
+    float w[V][4], bias[V];
     __device__ __forceinline__ void load(const ConvArgs& a, int c) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < V; ++i) {
             const float4 v = __ldg(reinterpret_cast<const float4*>(a.w) + c + i);
             w[i][0] = v.x; w[i][1] = v.y; w[i][2] = v.z; w[i][3] = v.w;
             bias[i] = 0.f;
         }
         if (a.bias) {
-            const float4 u = __ldg(reinterpret_cast<const float4*>(a.bias + c)), v = __ldg(reinterpret_cast<const float4*>(a.bias + c) + 1);
-            bias[0] = u.x; bias[1] = u.y; bias[2] = u.z; bias[3] = u.w;
-            bias[4] = v.x; bias[5] = v.y; bias[6] = v.z; bias[7] = v.w;
+#pragma unroll
+            for (int i = 0; i < V / 4; ++i) {
+                const float4 u = __ldg(reinterpret_cast<const float4*>(a.bias + c) + i);
+                bias[4 * i] = u.x; bias[4 * i + 1] = u.y; bias[4 * i + 2] = u.z; bias[4 * i + 3] = u.w;
+            }
         }
     }
-    __device__ __forceinline__ uint4 out(const float (&p0)[8], const float (&p1)[8], const float (&p2)[8], const float (&p3)[8]) const {
-        float y[8];
+    __device__ __forceinline__ ConvRow<V> out(const float (&p0)[V], const float (&p1)[V], const float (&p2)[V], const float (&p3)[V]) const {
+        float y[V];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < V; ++i) {
             float z = fmaf(w[i][0], p0[i], bias[i]);
             z = fmaf(w[i][1], p1[i], z);
             z = fmaf(w[i][2], p2[i], z);
             y[i] = silu(fmaf(w[i][3], p3[i], z));
         }
-        return make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        ConvRow<V> o;
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) o.r[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
+        return o;
     }
 };
 
 __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_constant__ ConvArgs a, int tiles, int cblocks) {
+    constexpr int V = 4;   // with 8 fewer warps are resident: 53 us for 4 ragged prompts of up to 2,048 x 8,192 channels, 48 with 4
     grid_dep_wait();
     grid_dep_launch();
     const int cb = blockIdx.x % cblocks;
     const int tl = (blockIdx.x / cblocks) % tiles;
     const int b = blockIdx.x / cblocks / tiles;
-    const int c = (cb * kConvThreads + threadIdx.x) * kConvVec;
+    const int c = (cb * kConvThreads + threadIdx.x) * V;
     if (c >= a.C) return;
     const int t0 = tl * kConvTile;
     const int len = seq_len(a.lens, b, a.n, a.status, tl == 0 && cb == 0 && threadIdx.x == 0);
@@ -71,51 +105,64 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
     const uint16_t* x = a.x + (int64_t)b * a.n * a.x_stride + c;
     uint16_t* st = a.state + (int64_t)b * 3 * a.C + c;
     uint16_t* out = a.out + (int64_t)b * a.n * a.C + c;
-    auto row = [&](int t) { return *reinterpret_cast<const uint4*>(x + (int64_t)t * a.x_stride); };
+    auto row = [&](int t) { return ConvRow<V>::load(x + (int64_t)t * a.x_stride); };
     const int end = min(t0 + kConvTile, len);
-    uint4 next[kConvRows], h[3];
+    ConvRow<V> next[kConvRows], h[3];
 #pragma unroll
     for (int i = 0; i < kConvRows; ++i)
         if (t0 + i < end) next[i] = row(t0 + i);
-    ConvWeights w;
+    ConvWeights<V> w;
     w.load(a, c);
     if (t0 == 0) {
 #pragma unroll
-        for (int j = 0; j < 3; ++j) h[j] = *reinterpret_cast<const uint4*>(st + (int64_t)j * a.C);
+        for (int j = 0; j < 3; ++j) h[j] = ConvRow<V>::load(st + (int64_t)j * a.C);
         // the last three rows of (state, x): row len + j of the two in sequence
 #pragma unroll
         for (int j = 0; j < 3; ++j) {
             const int i = len + j;
-            const uint4 v = i >= 3 ? row(i - 3) : (i == 1 ? h[1] : h[2]);
-            *reinterpret_cast<uint4*>(st + (int64_t)j * a.C) = v;
+            const ConvRow<V> v = i >= 3 ? row(i - 3) : (i == 1 ? h[1] : h[2]);
+            v.store(st + (int64_t)j * a.C);
         }
     } else {
 #pragma unroll
         for (int j = 0; j < 3; ++j) h[j] = row(t0 - 3 + j);
     }
-    float p0[8], p1[8], p2[8];
-    unpack8(h[0], p0);
-    unpack8(h[1], p1);
-    unpack8(h[2], p2);
-    for (int t = t0; t < end; t += kConvRows) {
-        uint4 cur[kConvRows];
+    float p0[V], p1[V], p2[V];
+    h[0].floats(p0);
+    h[1].floats(p1);
+    h[2].floats(p2);
+    uint16_t* o = out + (int64_t)t0 * a.C;
+    auto one = [&](const ConvRow<V>& r) {
+        float p3[V];
+        r.floats(p3);
+        w.out(p0, p1, p2, p3).store(o);
+        o += a.C;
 #pragma unroll
-        for (int i = 0; i < kConvRows; ++i) cur[i] = next[i];
+        for (int k = 0; k < V; ++k) {
+            p0[k] = p1[k];
+            p1[k] = p2[k];
+            p2[k] = p3[k];
+        }
+    };
+    int t = t0;
+    const uint16_t* xn = x + (int64_t)(t0 + kConvRows) * a.x_stride;
+    for (; t + 2 * kConvRows <= end; t += kConvRows) {   // these rows and the next are all there
+        ConvRow<V> cur[kConvRows];
 #pragma unroll
-        for (int i = 0; i < kConvRows; ++i)
-            if (t + kConvRows + i < end) next[i] = row(t + kConvRows + i);
+        for (int i = 0; i < kConvRows; ++i) {
+            cur[i] = next[i];
+            next[i] = ConvRow<V>::load(xn);
+            xn += a.x_stride;
+        }
+#pragma unroll
+        for (int i = 0; i < kConvRows; ++i) one(cur[i]);
+    }
+    for (; t < end; t += kConvRows) {
 #pragma unroll
         for (int i = 0; i < kConvRows; ++i) {
             if (t + i < end) {
-                float p3[8];
-                unpack8(cur[i], p3);
-                *reinterpret_cast<uint4*>(out + (int64_t)(t + i) * a.C) = w.out(p0, p1, p2, p3);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    p0[k] = p1[k];
-                    p1[k] = p2[k];
-                    p2[k] = p3[k];
-                }
+                one(next[i]);
+                if (t + kConvRows + i < end) next[i] = row(t + kConvRows + i);
             }
         }
     }
@@ -123,39 +170,40 @@ __global__ void __launch_bounds__(kConvThreads) gdn_conv_kernel(const __grid_con
 
 // n == 1: `seqs` sequences a thread, two at a time
 __global__ void __launch_bounds__(kConvThreads) gdn_conv_token_kernel(const __grid_constant__ ConvArgs a, int seqs, int cblocks) {
+    constexpr int V = 8;
     grid_dep_wait();
     grid_dep_launch();
     const int cb = blockIdx.x % cblocks;
     const int b0 = (blockIdx.x / cblocks) * seqs, b1 = min(b0 + seqs, a.B);
-    const int c = (cb * kConvThreads + threadIdx.x) * kConvVec;
+    const int c = (cb * kConvThreads + threadIdx.x) * V;
     if (c >= a.C) return;
-    ConvWeights w;
+    ConvWeights<V> w;
     w.load(a, c);
     for (int b = b0; b < b1; b += 2) {
-        uint4 x[2], h[2][3];
+        ConvRow<V> x[2], h[2][3];
         bool on[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             on[i] = b + i < b1 && seq_len(a.lens, b + i, 1, a.status, cb == 0 && threadIdx.x == 0) > 0;
             if (on[i]) {
-                x[i] = *reinterpret_cast<const uint4*>(a.x + (int64_t)(b + i) * a.x_stride + c);
+                x[i] = ConvRow<V>::load(a.x + (int64_t)(b + i) * a.x_stride + c);
 #pragma unroll
-                for (int j = 0; j < 3; ++j) h[i][j] = *reinterpret_cast<const uint4*>(a.state + ((int64_t)(b + i) * 3 + j) * a.C + c);
+                for (int j = 0; j < 3; ++j) h[i][j] = ConvRow<V>::load(a.state + ((int64_t)(b + i) * 3 + j) * a.C + c);
             }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (!on[i]) continue;
             uint16_t* st = a.state + (int64_t)(b + i) * 3 * a.C + c;
-            *reinterpret_cast<uint4*>(st) = h[i][1];
-            *reinterpret_cast<uint4*>(st + a.C) = h[i][2];
-            *reinterpret_cast<uint4*>(st + 2 * (int64_t)a.C) = x[i];
-            float p0[8], p1[8], p2[8], p3[8];
-            unpack8(h[i][0], p0);
-            unpack8(h[i][1], p1);
-            unpack8(h[i][2], p2);
-            unpack8(x[i], p3);
-            *reinterpret_cast<uint4*>(a.out + (int64_t)(b + i) * a.C + c) = w.out(p0, p1, p2, p3);
+            h[i][1].store(st);
+            h[i][2].store(st + a.C);
+            x[i].store(st + 2 * (int64_t)a.C);
+            float p0[V], p1[V], p2[V], p3[V];
+            h[i][0].floats(p0);
+            h[i][1].floats(p1);
+            h[i][2].floats(p2);
+            x[i].floats(p3);
+            w.out(p0, p1, p2, p3).store(a.out + (int64_t)(b + i) * a.C + c);
         }
     }
 }
@@ -276,15 +324,15 @@ __global__ void __launch_bounds__(kRecThreads) gdn_recurrent_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_gdn_conv(const ConvArgs& a, cudaStream_t stream) {
-    const int cblocks = (a.C / kConvVec + kConvThreads - 1) / kConvThreads;
+    auto blocks = [&](int v) { return (a.C / v + kConvThreads - 1) / kConvThreads; };
     if (a.n == 1) {
-        const int seqs = a.B >= 256 ? 4 : (a.B >= 64 ? 2 : 1);
+        const int seqs = a.B >= 256 ? 4 : (a.B >= 64 ? 2 : 1), cblocks = blocks(8);
         const int64_t grid = (int64_t)cblocks * ((a.B + seqs - 1) / seqs);
         if (grid > 0x7fffffffll) return cudaErrorNotSupported;
         PdlLaunch l((unsigned)grid, kConvThreads, 0, stream);
         return cudaLaunchKernelEx(&l.cfg, gdn_conv_token_kernel, a, seqs, cblocks);
     }
-    const int tiles = (a.n + kConvTile - 1) / kConvTile;
+    const int tiles = (a.n + kConvTile - 1) / kConvTile, cblocks = blocks(4);
     const int64_t grid = (int64_t)cblocks * tiles * a.B;
     if (grid > 0x7fffffffll) return cudaErrorNotSupported;
     PdlLaunch l((unsigned)grid, kConvThreads, 0, stream);
