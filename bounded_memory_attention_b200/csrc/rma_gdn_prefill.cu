@@ -31,8 +31,6 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 
-#include <type_traits>
-
 #include "rma_gdn.cuh"
 #include "sm100_ptx.cuh"
 
@@ -578,7 +576,6 @@ constexpr int kScanThreads = 512;
 // registers a thread after the split, of 128 at launch: 2 x 192 + 88 + 40 = 4 x 128
 constexpr int kRegsMain = 192, kRegsOut = 88, kRegsRest = 40;
 static_assert(2 * kRegsMain + kRegsOut + kRegsRest <= 4 * 128, "the split must fit what the launch has");
-static_assert(kStages == 3, "the issuing warp goes through the stages by name");
 static_assert(kScanSmem <= 227 * 1024, "shared memory per CTA");
 
 // Tensor memory columns; a half is 64 keys of the state, or 32 tokens of the rest.  A thread overwrites
@@ -590,8 +587,9 @@ static_assert(kScanSmem <= 227 * 1024, "shared memory per CTA");
 //   Q S0 [320, 384),  P U [384, 448)
 constexpr uint32_t kTmS = 0, kTmW = 128, kTmX = 192, kTmU = 256, kTmQ = 320, kTmP = 384, kTmCols = 512;
 
-// named barriers: a half's lane maxima offered by a warp to the other half's (8), the output warps
-constexpr int kBarPair = 1, kBarOut = 9;
+// named barriers: a half's lane maxima offered by a warp to the other half's (8), the output warps,
+// a warp and the other half's (4)
+constexpr int kBarPair = 1, kBarOut = 9, kBarBoth = 10;
 
 enum ScanBar {
     kbFull = 0,      // [3] the stage's loads landed (tx bytes)
@@ -740,10 +738,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             constexpr uint32_t id128t = ptx::idesc_f16_f32(128, 128, false, true);
             constexpr uint32_t kImage = kTile >> 4, kHalfRows = (32 * 128) >> 4, kTLo = kOffTLo >> 4, kP = kOffP >> 4;
             const uint32_t go = ptx::elect_one();
-            // One chunk, in a stage that is a constant: with it the operands are constants or uniform, and the
-            // warp spends few instructions on each product.  False when the CTA is abandoned.
-            auto chunk = [&](auto stage_c, int c) -> bool {
-                constexpr int st = decltype(stage_c)::value;
+            // (The loop over the chunks is not unrolled by stage: three copies of it crowd the other roles out of
+            // the instruction caches, which costs more than constant operands save.)
+            for (int c = 0; c < nc; ++c) {
+                const int st = c % kStages;
                 const uint32_t kb = smem_base + st * kStageBytes, tb = kb + kStageTP;
                 // low words of the descriptors: address and leading offset (the state's increment takes K by
                 // columns).  16 values of the rows of an image are 32 bytes: 2 in the address field
@@ -753,15 +751,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                     ptx::tc_fence_after();
                     return there;
                 };
-                if (!wait(kbFull + st, c / kStages)) return false;
+                if (!wait(kbFull + st, c / kStages)) break;
                 // the chunk before is complete: the scaled U lies where W goes
-                if (c > 0 && !wait(kbPDone, c - 1)) return false;
+                if (c > 0 && !wait(kbPDone, c - 1)) break;
                 // W, as the halves of the state arrive; the first half's tokens are done first
-                if (!wait(kbS, c)) return false;
+                if (!wait(kbS, c)) break;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)   // hi, then lo
                     ptx::mma_ts1(kTmW, kTmS + 8 * ks, dk + 2 * (ks & 3), id64, ks > 0, go);
-                if (!wait(kbS + 1, c)) return false;
+                if (!wait(kbS + 1, c)) break;
 #pragma unroll
                 for (int ht = 0; ht < 2; ++ht) {
 #pragma unroll
@@ -769,12 +767,12 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                         ptx::mma_ts1(kTmW + 32 * ht, kTmS + 64 + 8 * ks, dk + kImage + ht * kHalfRows + 2 * (ks & 3), id32, 1, go);
                     ptx::mma_commit1(&bars[kbWDone + ht], go);
                 }
-                if (c > 0 && !wait(kbO, c - 1)) return false;
+                if (c > 0 && !wait(kbO, c - 1)) break;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
                     ptx::mma_ts1(kTmQ, kTmS + 64 * (ks >> 2) + 8 * (ks & 3), dk + (2 + (ks >> 2)) * kImage + 2 * (ks & 3), id64, ks > 0, go);
                 // U: the first half's X for all tokens, which is all of the first half's U; then the second half's
-                if (!wait(kbX, c)) return false;
+                if (!wait(kbX, c)) break;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     ptx::mma_ts1(kTmU, kTmX + 8 * ks, dt + 2 * ks, id64, ks > 0, go);
@@ -782,7 +780,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                     ptx::mma_ts1(kTmU, kTmX + 8 * ks, dt + kTLo + 2 * ks, id64, 1, go);
                 }
                 ptx::mma_commit1(&bars[kbUDone], go);
-                if (!wait(kbX + 1, c)) return false;
+                if (!wait(kbX + 1, c)) break;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     const uint32_t t = dt + kHalfRows + 4 + 2 * ks;
@@ -792,7 +790,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                 }
                 ptx::mma_commit1(&bars[kbUDone + 1], go);
                 // the state's increment: the first half's tokens for all keys, then the second's for each half of them
-                if (!wait(kbU, c)) return false;
+                if (!wait(kbU, c)) break;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {   // 16 rows are 2 KiB
                     ptx::mma_ts1(kTmS, kTmW + 8 * ks, dd + 128 * ks, id128t, ks > 0, go);
@@ -801,7 +799,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks)
                     ptx::mma_ts1(kTmP, kTmU + 8 * ks, dt + kP + 2 * ks, id64, ks > 0, go);
-                if (!wait(kbU + 1, c)) return false;
+                if (!wait(kbU + 1, c)) break;
 #pragma unroll
                 for (int hk = 0; hk < 2; ++hk) {
 #pragma unroll
@@ -816,12 +814,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                 for (int ks = 0; ks < 2; ++ks)
                     ptx::mma_ts1(kTmP + 32, kTmU + 32 + 8 * ks, dt + kP + kHalfRows + 4 + 2 * ks, id32, 1, go);
                 ptx::mma_commit1(&bars[kbPDone], go);
-                return true;
-            };
-            for (int c = 0; c < nc; c += kStages) {
-                if (!chunk(std::integral_constant<int, 0>{}, c)) break;
-                if (c + 1 < nc && !chunk(std::integral_constant<int, 1>{}, c + 1)) break;
-                if (c + 2 < nc && !chunk(std::integral_constant<int, 2>{}, c + 2)) break;
             }
             ptx::mma_commit1(&bars[kbDrain], go);
             __syncwarp();
@@ -845,7 +837,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             const float inv_p = scal[kPS];
             ok = ptx::mbar_wait_warp(&bars[kbPDone], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int hl = 0; hl < 2; ++hl) {            // 16 columns
                 f2 is[2], iu[2];
 #pragma unroll
@@ -948,52 +940,44 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
         f2 S[32];   // times 2^es: keys 64 wg + 2 i, 2 i + 1
         int es;
         float* gs = a.state + ((int64_t)unit * kGdnDim + 64 * wg) * kGdnDim + row;
-        float smax = 0.f, vmax;
+        float smax = 0.f, vmax = 0.f;
         {
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = pack2(gs[2 * i * kGdnDim], gs[(2 * i + 1) * kGdnDim]);
 #pragma unroll
             for (int i = 0; i < 32; ++i) smax = absmax(smax, S[i]);
-            ok = ptx::mbar_wait_warp(&bars[kbFull], 0, abort_flag, a.status);
-            vmax = get_v(0);
-            offer(smax, vmax);
+            offer(smax, 0.f);
             take(smax, vmax);
+            ptx::named_bar_sync(kBarBoth + w, 64);   // both have taken, before the next offer
             es = scale_exponent(smax, 15);
             smax *= pow2(es);   // scaled, as the state is
             const f2 f = pack2(pow2(es), pow2(es));
 #pragma unroll
             for (int i = 0; i < 32; ++i) S[i] = mul2(S[i], f);
         }
-        auto put_state = [&](int c) {
-            if (wg == 0) exps[(c & 1) * 256 + row] = (int8_t)es;
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                uint32_t hi[16], lo[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) split2(S[16 * p + i], hi[i], lo[i]);
-                ptx::tmem_st16(tl + kTmS + 64 * wg + 16 * p, hi);
-                ptx::tmem_st16(tl + kTmS + 64 * wg + 32 + 16 * p, lo);
-            }
-            signal(kbS);
-        };
         constexpr float kCap = 1.2676506e30f;   // 2^100: a factor beyond it multiplies a zero, and must not be infinite
-        put_state(0);
-        for (int c = 0; c < nc; ++c) {
+        // Step -1 only brings the state and the first V in.
+#pragma unroll 1
+        for (int c = -1; c < nc; ++c) {
+          uint32_t x[32];
+          float ck = 1.f;
+          int es1 = es;
+          if (c >= 0) {
             const int st = c % kStages;
             const float* one = reinterpret_cast<const float*>(smem + st * kStageBytes + kStageTP + kOffScal);
             const float* scal = one + 32 * wg;   // this half's tokens
             // while W is computed: the bounds and the scales
-            if (c > 0) take(smax, vmax);
+            take(smax, vmax);
             const float inv_s = pow2(-es);
             smax *= inv_s;
             const float keep = one[kEC], bx = fmaf(one[kBW], smax, vmax);
             const int ex = scale_exponent(bx, 15), eu = scale_exponent(one[kBT] * bx, 15);
-            const int es1 = scale_exponent(fmaf(one[kBS], bx, keep * smax), 15);
+            es1 = scale_exponent(fmaf(one[kBS], bx, keep * smax), 15);
             const float fx = pow2(ex), from_x = pow2(-ex) * one[kTS];
             const float cw = -fminf(inv_s * fx, kCap);                // W to X's scale
             const float cu = fminf(pow2(eu) * from_x, kCap);          // U's accumulator to U's scale
             const float cd = fminf(pow2(es1) * from_x, kCap);         // and, with c3, to the new state's
-            const float ck = fminf(keep * inv_s * pow2(es1), kCap);   // the state to its new scale
+            ck = fminf(keep * inv_s * pow2(es1), kCap);               // the state to its new scale
             if (wg == 0) exps[(c & 1) * 256 + 128 + row] = (int8_t)eu;
             {
                 const f2 f = pack2(fx, fx);
@@ -1002,7 +986,6 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             }
             // X
             // (an abandoned CTA goes on through its barriers, on values that nobody uses)
-            uint32_t x[32];
             ok = ptx::mbar_wait_warp(&bars[kbWDone + wg], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmW + 32 * wg, x);
@@ -1048,16 +1031,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                 signal(kbU);
             }
             if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);   // (the output warps wait for the products)
+          }
             // while the increment is computed: the next chunk's V
             if (c + 1 < nc) {
                 ok = ptx::mbar_wait_warp(&bars[kbFull + (c + 1) % kStages], ((c + 1) / kStages) & 1, abort_flag, a.status) && ok;
                 vmax = get_v(c + 1);
             }
             // the state
-            ok = ptx::mbar_wait_warp(&bars[kbDDone + wg], c & 1, abort_flag, a.status) && ok;
-            ptx::tc_fence_after();
-            es = es1;
-            {
+            if (c >= 0) {
+                ok = ptx::mbar_wait_warp(&bars[kbDDone + wg], c & 1, abort_flag, a.status) && ok;
+                ptx::tc_fence_after();
+                es = es1;
                 const f2 k2 = pack2(ck, ck);
                 float m[2] = {0.f, 0.f};
 #pragma unroll
@@ -1074,7 +1058,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             }
             if (c + 1 < nc) {
                 offer(smax, vmax);
-                put_state(c + 1);
+                if (wg == 0) exps[((c + 1) & 1) * 256 + row] = (int8_t)es;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) split2(S[16 * p + i], hi[i], lo[i]);
+                    ptx::tmem_st16(tl + kTmS + 64 * wg + 16 * p, hi);
+                    ptx::tmem_st16(tl + kTmS + 64 * wg + 32 + 16 * p, lo);
+                }
+                signal(kbS);
             }
         }
         if (ok) {
