@@ -68,6 +68,15 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     lo = half2_bits(a - f.x, b - f.y);
 }
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+// The warp's index, in a register that is known to be the same in all lanes: what follows from it (roles,
+// barriers, rows) is computed once for the warp.
+__device__ __forceinline__ int warp_index() { return __reduce_max_sync(0xffffffffu, (int)(threadIdx.x >> 5)); }
+
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -102,6 +111,7 @@ __device__ __forceinline__ int piece_at(int row, int piece) { return row * 128 +
 // launch 1
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
+constexpr int kRowTop = 4;         // the largest value of a scaled row of K or Q is below 2^kRowTop
 constexpr int kHeadsAtOnce = 4;    // value heads whose gates are computed together, one per warp
 constexpr int kLd = kC + 4;        // row of a matrix that the tensor cores' fragments are read from
 
@@ -112,7 +122,7 @@ struct __align__(1024) PrepSmem {
         float prod[2][kC][kC];          // then K K^T and Q K^T, 16-byte pieces permuted (prod_at)
     };
     float T[2][kC][kLd];                // A, overwritten by its inverse block by block
-    float Gh[kHeadsAtOnce][kC], Gl[kHeadsAtOnce][kC];   // sums of g, as the sum of two floats
+    float Gh[kHeadsAtOnce][kC], Gl[kHeadsAtOnce][kC];   // sums of g log2(e), as the sum of two floats
     float beta[kHeadsAtOnce][kC];
     float rk[kC], rq[kC], ks[kC];       // row factors of K and Q, sums of |K|
     float kn[kC], qn[kC];               // norms of the rows with their factors
@@ -142,13 +152,24 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // d += A[16 x 8] B[8 x 8], A's rows kLd floats apart, B as fragment: b0 = B[lane % 4][lane / 4], b1 four rows on
-__device__ __forceinline__ void mma_fp32(float (&d)[4], const float* A, float b0, float b1, int lane) {
+struct Acc {   // the products of the high parts, and the two corrections
+    float d[4], u[4], v[4];
+    __device__ __forceinline__ Acc() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = u[i] = v[i] = 0.f;
+    }
+    __device__ __forceinline__ void sum(float (&r)[4]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = d[i] + (u[i] + v[i]);
+    }
+};
+__device__ __forceinline__ void mma_fp32(Acc& acc, const float* A, float b0, float b1, int lane) {
     const float* p = A + (lane >> 2) * kLd + (lane & 3);
     const Tf a0 = tf_split(p[0]), a1 = tf_split(p[8 * kLd]), a2 = tf_split(p[4]), a3 = tf_split(p[8 * kLd + 4]);
     const Tf c0 = tf_split(b0), c1 = tf_split(b1);
-    mma_tf32(d, a0.lo, a1.lo, a2.lo, a3.lo, c0.hi, c1.hi);
-    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, c0.lo, c1.lo);
-    mma_tf32(d, a0.hi, a1.hi, a2.hi, a3.hi, c0.hi, c1.hi);
+    mma_tf32(acc.u, a0.lo, a1.lo, a2.lo, a3.lo, c0.hi, c1.hi);
+    mma_tf32(acc.v, a0.hi, a1.hi, a2.hi, a3.hi, c0.lo, c1.lo);
+    mma_tf32(acc.d, a0.hi, a1.hi, a2.hi, a3.hi, c0.hi, c1.hi);
 }
 // rows 8 half .. of a 16 x 8 accumulator, as a B fragment
 __device__ __forceinline__ void as_b(const float (&d)[4], int half, int lane, float& b0, float& b1) {
@@ -187,56 +208,66 @@ __device__ __forceinline__ void invert(float (*T)[kLd], int warp, int lane, int 
             for (int i = 0; i < 16; ++i) T[q + i][q + j] = x[i];
             __syncwarp();
         }
+        Acc y[2], z[2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-            float d[4] = {}, e[4] = {};
+        for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
             for (int ks = nt; ks < 2; ++ks) {   // T11's columns 8 nt .. are 0 above row 8 nt
                 const float* t = &T[o + 8 * ks + br][o + 8 * nt + bc];
-                mma_fp32(d, &T[o + 16][o + 8 * ks], t[0], t[4 * kLd], lane);
+                mma_fp32(y[nt], &T[o + 16][o + 8 * ks], t[0], t[4 * kLd], lane);
             }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            float d[4];
+            y[nt].sum(d);
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 float b0, b1;
                 as_b(d, ks, lane, b0, b1);
-                mma_fp32(e, &T[o + 16][o + 16 + 8 * ks], b0, b1, lane);
+                mma_fp32(z[nt], &T[o + 16][o + 16 + 8 * ks], b0, b1, lane);
             }
-            // columns 8 nt .. of A21 are not needed any more: the other half's products take their own
-            if (nt == 0) __syncwarp();
-            put_neg(nt == 0 ? &T[o][o + 16] : &T[o + 16][o + 8], e, lane);
         }
-        // (the first half waits in the zero block above the diagonal, since the second reads all of A21)
-        __syncwarp();
-        {
-            const int r = lane >> 1, h = (lane & 1) * 4;
-            float4* from = reinterpret_cast<float4*>(&T[o + r][o + 16 + h]);
-            *reinterpret_cast<float4*>(&T[o + 16 + r][o + h]) = *from;
-            *from = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncwarp();   // A21 has been read
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+            float e[4];
+            z[nt].sum(e);
+            put_neg(&T[o + 16][o + 8 * nt], e, lane);
         }
     }
     ptx::named_bar_sync(bar, 128);
     {
         const int n0 = 8 * warp;
-        float d[2][4] = {}, e[2][4] = {};
+        float d[2][4];
+        {
+            Acc y[2];
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-            if (ks >= warp) {
-                const float* t = &T[8 * ks + br][n0 + bc];
-                const float b0 = t[0], b1 = t[4 * kLd];
+            for (int ks = 0; ks < 4; ++ks)
+                if (ks >= warp) {
+                    const float* t = &T[8 * ks + br][n0 + bc];
+                    const float b0 = t[0], b1 = t[4 * kLd];
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) mma_fp32(d[mt], &T[32 + 16 * mt][8 * ks], b0, b1, lane);
-            }
+                    for (int mt = 0; mt < 2; ++mt) mma_fp32(y[mt], &T[32 + 16 * mt][8 * ks], b0, b1, lane);
+                }
+            y[0].sum(d[0]);
+            y[1].sum(d[1]);
+        }
         ptx::named_bar_sync(bar, 128);   // A21 has been read
+        Acc z[2];
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             float b0, b1;
             as_b(d[ks >> 1], ks & 1, lane, b0, b1);
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
-                if (ks < 2 * mt + 2) mma_fp32(e[mt], &T[32 + 16 * mt][32 + 8 * ks], b0, b1, lane);
+                if (ks < 2 * mt + 2) mma_fp32(z[mt], &T[32 + 16 * mt][32 + 8 * ks], b0, b1, lane);
         }
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) put_neg(&T[32 + 16 * mt][n0], e[mt], lane);
+        for (int mt = 0; mt < 2; ++mt) {
+            float e[4];
+            z[mt].sum(e);
+            put_neg(&T[32 + 16 * mt][n0], e, lane);
+        }
     }
     ptx::named_bar_sync(bar, 128);
 }
@@ -244,7 +275,7 @@ __device__ __forceinline__ void invert(float (*T)[kLd], int warp, int lane, int 
 __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
     extern __shared__ uint8_t smem_raw[];
     PrepSmem& s = *reinterpret_cast<PrepSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int kh = blockIdx.x % a.HK;
     const int b = (blockIdx.x / a.HK) % a.B;
     const int c = blockIdx.x / a.HK / a.B;
@@ -274,14 +305,15 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                 gates(a.a[at], a.b[at], alpha, dt, g[i], bt[i]);
             }
         }
-        const double own = (double)g[0] + (double)g[1];
+        // sums of g log2(e): decays are powers of two from here on
+        const double e0 = (double)g[0] * 1.4426950408889634, e1 = (double)g[1] * 1.4426950408889634, own = e0 + e1;
         double run = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const double up = __shfl_up_sync(0xffffffffu, run, o);
             if (lane >= o) run += up;
         }
-        const double G[2] = {run - own + (double)g[0], run};
+        const double G[2] = {run - own + e0, run};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float hi = (float)G[i];
@@ -307,10 +339,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
             }
         }
         head_gates(0);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-            const int m = it >> 1, row = (it & 1) * 32 + row0;
-            float x[16];
+        // (the four rows of these lanes go in step, so that their shuffles overlap)
+        float mx[4], ss[4], sa[4];
+        auto values = [&](int it, float (&x)[16]) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const float2 p0 = unpack_bf16(raw[it][i].x), p1 = unpack_bf16(raw[it][i].y);
@@ -318,24 +349,32 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                 x[8 * i] = p0.x; x[8 * i + 1] = p0.y; x[8 * i + 2] = p1.x; x[8 * i + 3] = p1.y;
                 x[8 * i + 4] = p2.x; x[8 * i + 5] = p2.y; x[8 * i + 6] = p3.x; x[8 * i + 7] = p3.y;
             }
-            float mx = 0.f;
+        };
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, fabsf(x[i]));
+        for (int it = 0; it < 4; ++it) {
+            float x[16];
+            values(it, x);
+            mx[it] = 0.f;
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const int e = scale_exponent(mx, 8);
-            const float f = pow2(e), inv = pow2(-e);
-            float ss = 0.f, sa = 0.f;
+            for (int i = 0; i < 16; i += 2) asm("max.abs.f32 %0, %0, %1, %2;\n" : "+f"(mx[it]) : "f"(x[i]), "f"(x[i + 1]));
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) mx[it] = fmaxf(mx[it], __shfl_xor_sync(0xffffffffu, mx[it], o));
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int m = it >> 1, row = (it & 1) * 32 + row0;
+            const float f = pow2(scale_exponent(mx[it], kRowTop));
+            float x[16];
+            values(it, x);
+            ss[it] = 0.f;
+            sa[it] = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 x[i] *= f;
-                ss = fmaf(x[i], x[i], ss);
-                sa += fabsf(x[i]);
-            }
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) {
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                sa += __shfl_xor_sync(0xffffffffu, sa, o);
+                ss[it] = fmaf(x[i], x[i], ss[it]);
+                sa[it] += fabsf(x[i]);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -345,23 +384,39 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                 *reinterpret_cast<uint4*>(s.kq + at) = v;
                 *reinterpret_cast<uint4*>(kq_out + at) = v;
             }
-            if (l8 == 0) {
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                ss[it] += __shfl_xor_sync(0xffffffffu, ss[it], o);
+                sa[it] += __shfl_xor_sync(0xffffffffu, sa[it], o);
+            }
+        // lanes 0-3 of the eight finish a row each
+        {
+            float ssr = ss[0], sar = sa[0], mxr = mx[0];
+#pragma unroll
+            for (int it = 1; it < 4; ++it)
+                if (l8 == it) ssr = ss[it], sar = sa[it], mxr = mx[it];
+            if (l8 < 4) {
+                const int m = l8 >> 1, row = (l8 & 1) * 32 + row0, e = scale_exponent(mxr, kRowTop);
+                const float f = pow2(e), inv = pow2(-e);
                 // 1 / sqrt(sum x^2 + eps) times the row's scale; the sum is of scaled values, so the one
                 // form keeps large rows from overflowing and the other rows far below eps from NaN
                 float r = inv;
                 if (a.l2norm) {
-                    if (e <= 60 || a.l2_eps == 0.f) r = 1.f / sqrtf(ss + a.l2_eps * f * f);
-                    else r = inv / sqrtf(ss * inv * inv + a.l2_eps);
+                    if (e <= 60 || a.l2_eps == 0.f) r = 1.f / sqrtf(ssr + a.l2_eps * f * f);
+                    else r = inv / sqrtf(ssr * inv * inv + a.l2_eps);
                 }
                 if (row >= valid) r = 0.f;
                 if (m) {
                     r *= a.scale;
                     s.rq[row] = r;
-                    s.qn[row] = fabsf(r) * sqrtf(ss);
+                    s.qn[row] = fabsf(r) * sqrtf(ssr);
                 } else {
                     s.rk[row] = r;
-                    s.ks[row] = sa;
-                    s.kn[row] = r * sqrtf(ss);
+                    s.ks[row] = sar;
+                    s.kn[row] = r * sqrtf(ssr);
                 }
             }
         }
@@ -438,14 +493,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                 float cf[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
-                    cf[x] = s.rk[8 * p + x] * __expf((rh - Gh[8 * p + x]) + (rl - Gl[8 * p + x]));
+                    cf[x] = s.rk[8 * p + x] * ex2((rh - Gh[8 * p + x]) + (rl - Gl[8 * p + x]));
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int i = (gt >> 3) + 16 * k;
                     if ((i >> 3) == p) continue;   // the diagonal's
                     float A[8], P[8];
                     if (p < (i >> 3)) {
-                        const float ei = __expf((Gh[i] - rh) + (Gl[i] - rl));
+                        const float ei = ex2((Gh[i] - rh) + (Gl[i] - rl));
                         const float fa = beta[i] * s.rk[i] * ei, fp = s.rq[i] * p_scale * ei;
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
@@ -476,7 +531,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int j = j0 + x;
-                    const float d = s.rk[j] * __expf((gh - Gh[j]) + (gl - Gl[j]));
+                    const float d = s.rk[j] * ex2((gh - Gh[j]) + (gl - Gl[j]));
                     A[x] = j < i ? fa * d * kk[x] : 0.f;
                     P[x] = j <= i ? fp * d * qk[x] : 0.f;
                 }
@@ -485,8 +540,8 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                     make_uint2(half2_bits(P[0], P[1]), half2_bits(P[2], P[3]));
             }
             if (gt < kC) {
-                const float since = __expf(Gh[gt] + Gl[gt]);
-                const float until = __expf((Gh[kC - 1] - Gh[gt]) + (Gl[kC - 1] - Gl[gt]));
+                const float since = ex2(Gh[gt] + Gl[gt]);
+                const float until = ex2((Gh[kC - 1] - Gh[gt]) + (Gl[kC - 1] - Gl[gt]));
                 scal[kC1 + gt] = s.c1[grp][gt] = since * s.rk[gt];
                 scal[kC2 + gt] = since * s.rq[gt];
                 scal[kC3 + gt] = s.c3[grp][gt] = until * s.rk[gt];
@@ -495,41 +550,50 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
             if (gt == 0) s.tmax[grp] = 0u;
             ptx::named_bar_sync(bar, 128);
             invert(T, gw, lane, bar);
-            // T with beta's columns: its largest value, its rows' sums; scaled, split, to the workspace
+            // T with beta's columns, its rows' sums; scaled, split, to the workspace.  With normed keys no value
+            // of it exceeds 1: u_i for a single x_j = 1 is beta_i k_i . (contractions) k_j beta_j.
             {
-                float v[4][8], mx = 0.f;
                 const float4 b0 = *reinterpret_cast<const float4*>(beta + 8 * p), b1 = *reinterpret_cast<const float4*>(beta + 8 * p + 4);
+                float tmax = 1.f;
+                if (!a.l2norm) {
+                    float mx = 0.f;
+#pragma unroll 1
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 t0 = *reinterpret_cast<const float4*>(&T[(gt >> 3) + 16 * k][8 * p]);
+                        const float4 t1 = *reinterpret_cast<const float4*>(&T[(gt >> 3) + 16 * k][8 * p + 4]);
+                        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(t0.x * b0.x), fabsf(t0.y * b0.y)), fmaxf(fabsf(t0.z * b0.z), fabsf(t0.w * b0.w))));
+                        mx = fmaxf(mx, fmaxf(fmaxf(fabsf(t1.x * b1.x), fabsf(t1.y * b1.y)), fmaxf(fabsf(t1.z * b1.z), fabsf(t1.w * b1.w))));
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    if (lane == 0) atomicMax(&s.tmax[grp], __float_as_uint(mx));
+                    ptx::named_bar_sync(bar, 128);
+                    tmax = __uint_as_float(s.tmax[grp]);
+                }
+                const int e = scale_exponent(tmax, 8);
+                const float sc = pow2(e);
+                float sum[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int i = (gt >> 3) + 16 * k;
                     const float4 t0 = *reinterpret_cast<const float4*>(&T[i][8 * p]), t1 = *reinterpret_cast<const float4*>(&T[i][8 * p + 4]);
-                    v[k][0] = t0.x * b0.x; v[k][1] = t0.y * b0.y; v[k][2] = t0.z * b0.z; v[k][3] = t0.w * b0.w;
-                    v[k][4] = t1.x * b1.x; v[k][5] = t1.y * b1.y; v[k][6] = t1.z * b1.z; v[k][7] = t1.w * b1.w;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        mx = fmaxf(mx, fabsf(v[k][x]));
-                        sum += fabsf(v[k][x]);
-                    }
-#pragma unroll
-                    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                    if (p == 0) s.tsum[grp][i] = sum;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                if (lane == 0) atomicMax(&s.tmax[grp], __float_as_uint(mx));
-                ptx::named_bar_sync(bar, 128);
-                const int e = scale_exponent(__uint_as_float(s.tmax[grp]), 8);
-                const float sc = pow2(e);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = (gt >> 3) + 16 * k;
+                    const float v[8] = {t0.x * b0.x, t0.y * b0.y, t0.z * b0.z, t0.w * b0.w, t1.x * b1.x, t1.y * b1.y, t1.z * b1.z, t1.w * b1.w};
+                    sum[k] = 0.f;
                     uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) split2(v[k][2 * x] * sc, v[k][2 * x + 1] * sc, hi[x], lo[x]);
+                    for (int x = 0; x < 4; ++x) {
+                        sum[k] += fabsf(v[2 * x]) + fabsf(v[2 * x + 1]);
+                        split2(v[2 * x] * sc, v[2 * x + 1] * sc, hi[x], lo[x]);
+                    }
                     *reinterpret_cast<uint4*>(out + piece_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(out + kOffTLo + piece_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
+#pragma unroll
+                for (int o = 4; o > 0; o >>= 1)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+                if (p < 4) s.tsum[grp][(gt >> 3) + 16 * p] = p == 0 ? sum[0] : p == 1 ? sum[1] : p == 2 ? sum[2] : sum[3];
+                ptx::named_bar_sync(bar, 128);
                 if (gw == 0) {
                     float bw = 0.f, bt = 0.f, bs = 0.f;
 #pragma unroll
@@ -550,7 +614,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                         scal[kPS] = pow2(-ep);
                         scal[kBW] = bw;
                         scal[kBT] = bt;
-                        scal[kBS] = bs * 256.f;   // a scaled key's values are below 256
+                        scal[kBS] = bs * (1 << kRowTop);
                     }
                 }
             }
@@ -670,7 +734,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     // the same place as a shared-memory address and as a pointer
     const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
     const int unit = blockIdx.x, b = unit / a.HV, h = unit % a.HV, kh = h / (a.HV / a.HK);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kScanBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kScanBars);

@@ -275,6 +275,28 @@ def test_block_of_lengths(n, lens):
     assert rma.gdn_get_status(st) == 0
 
 
+def test_block_of_more_heads_than_multiprocessors():
+    """180 (sequence, head) pairs of very different lengths: a multiprocessor takes several, one after another."""
+    B, n = 60, 70
+    lens = si.uniform_int((B,), 0, n, 71).to(torch.int32)
+    lens[:6] = torch.tensor([n, 0, 64, 65, 1, 0])
+    rma, st, d, x = delta_case(B, n, 1, 3, seed=72)
+    out = torch.full((B, n, 3, 128), 7.0, dtype=BF, device="cuda")
+    rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, st.workspace(n), lens=lens.cuda())
+    past = delta_check(out, st.delta[0], x, 1, lens=lens.numpy())
+    assert (f64(out)[past] == 7.0).all() and torch.equal(st.delta[0, 1].cpu(), x["state"][1])
+    again = torch.full_like(out, 7.0)   # without lengths of 0, in the batch's own order
+    few = rma.GdnState(rma.GdnConfig(batch=1, n_k_heads=1, n_v_heads=3))
+    for b in (0, 2, 3):
+        few.delta[0].copy_(d["state"][b:b + 1])
+        m = int(lens[b])
+        o = torch.empty(1, m, 3, 128, dtype=BF, device="cuda")
+        p = {k: d[k][b:b + 1, :m].contiguous() for k in ("qkv", "a", "b")}
+        rma.gdn_prefill(few, 0, p["qkv"], p["a"], p["b"], d["a_log"], d["dt_bias"], o, few.workspace(m))
+        again[b, :m] = o[0]
+        assert torch.equal(again[b], out[b]) and torch.equal(few.delta[0, 0], st.delta[0, b])
+
+
 def test_lengths_out_of_range_are_clamped_and_reported():
     rma, st, d, x = delta_case(2, 70, 1, 2, seed=80)
     out = torch.full((2, 70, 2, 128), 7.0, dtype=BF, device="cuda")
