@@ -96,6 +96,11 @@ __device__ __forceinline__ void stsm4_trans(uint32_t addr, uint32_t r0, uint32_t
                  "r"(r2), "r"(r3)
                  : "memory");
 }
+// Ask for `bytes` (a multiple of 16) at a 16-byte aligned global address to be brought into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes)
+                 : "memory");
+}
 // TMA store of one box from shared memory (bulk-group completion).
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(
@@ -741,6 +746,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     float* maxima = reinterpret_cast<float*>(smem + kScanMax);
     int8_t* exps = reinterpret_cast<int8_t*>(smem + kScanExp);
+    // This unit's state towards L2, before anything is waited for.
+    const float* state = a.state + (int64_t)unit * kGdnDim * kGdnDim;
+    if (tid == 0) prefetch_l2(state, kGdnDim * kGdnDim * 4);
     grid_dep_wait();
     grid_dep_launch();
     const int len = seq_len(a.lens, b, a.n, a.status, false);
@@ -777,6 +785,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
             for (int c = 0; c < nc; ++c) {
                 const int st = c % kStages;
                 if (c >= kStages && !ptx::mbar_wait_warp(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag, a.status)) break;
+                // the state and the first chunk come first: they are what the start waits for
+                if (c == 1 && !ptx::mbar_wait_warp(&bars[kbS], 0, abort_flag, a.status)) break;
                 issued = c + 1;
                 uint8_t* stage = smem + st * kStageBytes;
                 if (lane == 0) {
