@@ -31,19 +31,19 @@ def _stream(stream, index: int) -> int:
     return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
-def _tensor(t, dtype, name: str, index: int) -> None:
-    """`t` is a tensor of `dtype` on CUDA device `index`."""
+def _wrong(t, dtype, name: str, index: int):
+    """What is wrong with `t` as a tensor of `dtype` on CUDA device `index`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+        return TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the state on device {index}")
+        return TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return ValueError(f"{name} is on {t.device}, the state on device {index}")
 
 
 def _dense(t, dtype, numel: int, name: str, index: int) -> int:
     """The address of a contiguous tensor."""
-    _tensor(t, dtype, name, index)
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or t.get_device() != index:
+        raise _wrong(t, dtype, name, index)
     if t.numel() != numel:
         raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
     if not t.is_contiguous():
@@ -54,24 +54,25 @@ def _dense(t, dtype, numel: int, name: str, index: int) -> int:
 def _rows(t, dtype, batch: int, n: int, inner: tuple, name: str, index: int):
     """(address, elements from one token to the next) of a [batch, n, *inner] tensor (or
     [batch, *inner] for n == 1) whose tokens are contiguous rows, evenly spaced over the batch too."""
-    _tensor(t, dtype, name, index)
-    shape, strides = t.shape, t.stride()
-    if n == 1 and shape == (batch, *inner):
-        shape, strides = (batch, 1, *inner), (strides[0], strides[0], *strides[1:])
-    if shape != (batch, n, *inner):
-        raise ValueError(f"{name} has shape {list(t.shape)}, expected {[batch, n, *inner]}")
-    row = 1
-    for size, step in zip(reversed(inner), reversed(strides[2:])):
-        if size != 1 and step != row:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or t.get_device() != index:
+        raise _wrong(t, dtype, name, index)
+    row = inner[0] if len(inner) == 1 else inner[0] * inner[1]
+    shape = t.shape
+    if shape != (batch, n, *inner) and not (n == 1 and shape == (batch, *inner)):
+        raise ValueError(f"{name} has shape {list(shape)}, expected {[batch, n, *inner]}")
+    if t.is_contiguous():
+        return t.data_ptr(), row
+    strides = t.stride()
+    step = 1
+    for size, stride in zip(reversed(inner), reversed(strides)):
+        if size != 1 and stride != step:
             raise ValueError(f"{name}: the values of a token must be contiguous")
-        row *= size
-    if n > 1:
-        step = strides[1]
-        if batch > 1 and strides[0] != n * step:
-            raise ValueError(f"{name}: the tokens must be evenly spaced over the whole batch")
-    else:
-        step = strides[0] if batch > 1 else row
-    return t.data_ptr(), step
+        step *= size
+    if n == 1:
+        return t.data_ptr(), strides[0] if batch > 1 else row
+    if batch > 1 and strides[0] != n * strides[1]:
+        raise ValueError(f"{name}: the tokens must be evenly spaced over the whole batch")
+    return t.data_ptr(), strides[1]
 
 
 def _tokens(t, batch: int, dims: int, name: str) -> int:
