@@ -639,6 +639,7 @@ constexpr int kScanBar = kStages * kStageBytes;
 constexpr int kScanMax = kScanBar + 256;                  // lane maxima: [state, V][2 halves][128]
 constexpr int kScanExp = kScanMax + 2 * 2 * 128 * 4;      // exponents of scales, for the output warps: [2 chunks][S0, U][128]
 constexpr int kScanSmem = kScanExp + 2 * 2 * 128 + 1024;
+constexpr int kMaxOrder = 64;                             // sequences that are ordered by length
 // warps 0-3 and 4-7: state, X and U, by halves; warps 8-11: outputs; warp 12 loads, warp 13 issues the products
 constexpr int kWarpOut = 8, kWarpLoad = 12, kWarpMma = 13;
 constexpr int kScanThreads = 512;
@@ -740,17 +741,37 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (smem_base - ptx::smem_u32(smem_raw));
     const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-    const int unit = blockIdx.x, b = unit / a.HV, h = unit % a.HV, kh = h / (a.HV / a.HK);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kScanBar);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kScanBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     float* maxima = reinterpret_cast<float*>(smem + kScanMax);
     int8_t* exps = reinterpret_cast<int8_t*>(smem + kScanExp);
-    // This unit's state towards L2, before anything is waited for.
-    const float* state = a.state + (int64_t)unit * kGdnDim * kGdnDim;
-    if (tid == 0) prefetch_l2(state, kGdnDim * kGdnDim * 4);
+    // More heads than multiprocessors and lengths that differ: the longest sequences' CTAs first, so that what
+    // is dealt out last is short.
+    const int h = blockIdx.x % a.HV, kh = h / (a.HV / a.HK);
+    int b = blockIdx.x / a.HV;
+    const bool ordered = a.lens && a.B > 1 && a.B <= kMaxOrder && (int)gridDim.x > a.sm_count;
+    if (!ordered && tid == 0)   // the state towards L2, before anything is waited for
+        prefetch_l2(a.state + (int64_t)blockIdx.x * kGdnDim * kGdnDim, kGdnDim * kGdnDim * 4);
     grid_dep_wait();
     grid_dep_launch();
+    if (ordered) {
+        int* ls = reinterpret_cast<int*>(smem);
+        if (tid < a.B) ls[tid] = seq_len(a.lens, tid, a.n, a.status, false);
+        __syncthreads();
+        if (tid < a.B) {
+            const int mine = ls[tid];
+            int rank = 0;
+            for (int j = 0; j < a.B; ++j) rank += ls[j] > mine || (ls[j] == mine && j < tid);
+            if (rank == b) ls[kMaxOrder] = tid;
+        }
+        __syncthreads();
+        b = ls[kMaxOrder];
+        __syncthreads();   // before the stages take this memory
+        if (tid == 0) prefetch_l2(a.state + ((int64_t)b * a.HV + h) * kGdnDim * kGdnDim, kGdnDim * kGdnDim * 4);
+    }
+    b = __reduce_max_sync(0xffffffffu, b);   // known to be the same in all lanes
+    const int unit = b * a.HV + h;
     const int len = seq_len(a.lens, b, a.n, a.status, false);
     if (len == 0) return;
     const int nc = (len + kC - 1) / kC;
@@ -1183,7 +1204,8 @@ size_t gdn_prefill_workspace_bytes(const rma_gdn_config& c, int n) {
 }
 
 cudaError_t launch_gdn_prefill(const DeltaArgs& a, cudaStream_t stream) {
-    if (a.n < kGdnChunkedFrom) return launch_gdn_recurrent(a, stream);
+    const bool few = (int64_t)a.B * a.HV * 4 <= a.sm_count;
+    if (a.n < (few ? kGdnChunkedFromFew : kGdnChunkedFrom)) return launch_gdn_recurrent(a, stream);
     const int NC = (a.n + kC - 1) / kC;
     const int64_t grid = (int64_t)NC * a.B * a.HK;
     if (grid > 0x7fffffffll) return cudaErrorNotSupported;
