@@ -223,8 +223,8 @@ int check_layer(const State* s, int layer) {
 
 }  // namespace
 
-EncodeTiledFn encode_tiled_fn() {
-    static EncodeTiledFn fn = nullptr;
+TensorMapEncodeFn tensor_map_encode() {
+    static TensorMapEncodeFn fn = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
         void* p = nullptr;
@@ -232,7 +232,7 @@ EncodeTiledFn encode_tiled_fn() {
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
+            fn = reinterpret_cast<TensorMapEncodeFn>(p);
     });
     return fn;
 }

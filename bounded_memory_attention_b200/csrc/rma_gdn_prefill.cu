@@ -1183,7 +1183,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
 
 // A 2-D BF16 tensor of `rows` rows of `cols` values, boxes of bc columns x 64 rows.
 bool make_map2(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t bc, CUtensorMapSwizzle swizzle) {
-    EncodeTiledFn fn = encode_tiled_fn();
+    TensorMapEncodeFn fn = tensor_map_encode();
     if (!fn) return false;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * 2};

@@ -144,10 +144,10 @@ cudaError_t launch_quantize_layer(const LayerView& dst, const LayerView& src, cu
 size_t prefill_workspace_bytes(const rma_config& cfg, int n_tok);
 
 // cuTensorMapEncodeTiled through the driver entry point, or null.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+using TensorMapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn encode_tiled_fn();
+TensorMapEncodeFn tensor_map_encode();
 
 // ---- the layers around RMA attention (rma_qk_norm_rope, rma_gdn_*) ----
 

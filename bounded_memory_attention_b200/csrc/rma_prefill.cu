@@ -970,7 +970,23 @@ __global__ void __launch_bounds__(kCopyThreads) prefill_admit_copy_kernel(const 
 
 // ---- host side: tensor maps through the driver entry point ----
 
-EncodeTiledFn encode_fn() { return encode_tiled_fn(); }
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
 
 // 3-D BF16 tensor [d2][d1][256] with the given strides (bytes) for dims 1 and 2,
 // box (64, box1, box2), 128-byte swizzle, zero fill outside the tensor.
