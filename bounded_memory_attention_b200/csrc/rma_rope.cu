@@ -9,7 +9,8 @@
 // they are in flight; the sum of squares is one warp reduction.  A product of a far position and a
 // frequency has an absolute error of half an ulp of the angle, 0.008 rad at 2^18 in FP32, so the product
 // and its reduction to a fraction of a turn are in FP64; the fraction's sine and cosine then need FP32
-// only.  Pairs that lie in two lanes meet in the warp's row of shared memory.
+// only.  Partners in another lane come by shuffles, or through the warp's row of shared memory where a lane's
+// eight values do not have one side (rotary_dim / 2 not a multiple of 8).
 #include <cuda_bf16.h>
 
 #include "rma_internal.cuh"
@@ -32,8 +33,13 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Where pair p of a half-split rotation lies in the tables: a lane takes eight in a row, as two fours, and the
+// lanes' first fours lie side by side (eight in a row each put all lanes on four banks: 8-way conflicts, which
+// held 2,048 tokens to 20 us).
+__device__ __forceinline__ int at_pair(int p) { return ((p >> 2) & 1) * 64 + ((p >> 3) << 2) + (p & 3); }
+
 template <int T>   // tokens of a CTA
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ __align__(16) float cs[T][kHeadDim / 2], sn[T][kHeadDim / 2];
     __shared__ __align__(16) float rows[kHeads][kHeadDim];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -68,7 +74,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
             pos = (int64_t)max(c, 0) + (tok - b * a.n);
         }
         const double turns = (double)pos * (a.inv_freq[f] * 0.15915494309189533577);   // 1 / (2 pi)
-        sincospif(2.f * (float)(turns - rint(turns)), &sn[t][f], &cs[t][f]);
+        const int at = a.interleaved ? f : at_pair(f);
+        sincospif(2.f * (float)(turns - rint(turns)), &sn[t][at], &cs[t][at]);
     }
     __syncthreads();
 
@@ -104,31 +111,32 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
                 }
             }
         } else if (half > 0) {
-            float4* row = reinterpret_cast<float4*>(rows[warp]) + 2 * lane;
-            __syncwarp();   // the token before has been read
-            row[0] = make_float4(x[0], x[1], x[2], x[3]);
-            row[1] = make_float4(x[4], x[5], x[6], x[7]);
-            __syncwarp();
-            if ((half & 7) == 0) {   // a lane's values have one side each, and their partners are eight in a row
-                if (d0 < 2 * half) {
-                    const bool first = d0 < half;
-                    const int p = first ? d0 : d0 - half;
-                    const float4* other = reinterpret_cast<const float4*>(rows[warp] + (first ? d0 + half : p));
-                    const float4 o0 = other[0], o1 = other[1];
-                    const float4 c0 = *reinterpret_cast<const float4*>(&cs[t][p]), c1 = *reinterpret_cast<const float4*>(&cs[t][p + 4]);
-                    const float4 s0 = *reinterpret_cast<const float4*>(&sn[t][p]), s1 = *reinterpret_cast<const float4*>(&sn[t][p + 4]);
-                    const float y[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+            if ((half & 7) == 0) {   // a lane's values have one side each, and their partners are one lane's
+                const bool first = d0 < half, mine = d0 < 2 * half;
+                const int other = mine ? (first ? lane + half / 8 : lane - half / 8) : lane;
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, x[i], other);
+                if (mine) {
+                    const int p = (first ? d0 : d0 - half) >> 1;   // eight pairs, in two fours (at_pair)
+                    const float4 c0 = *reinterpret_cast<const float4*>(&cs[t][p]), c1 = *reinterpret_cast<const float4*>(&cs[t][p + 64]);
+                    const float4 s0 = *reinterpret_cast<const float4*>(&sn[t][p]), s1 = *reinterpret_cast<const float4*>(&sn[t][p + 64]);
                     const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
                     const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = first ? x[i] * c[i] - y[i] * s[i] : x[i] * c[i] + y[i] * s[i];
                 }
             } else {
+                float4* row = reinterpret_cast<float4*>(rows[warp]) + 2 * lane;
+                __syncwarp();   // the token before has been read
+                row[0] = make_float4(x[0], x[1], x[2], x[3]);
+                row[1] = make_float4(x[4], x[5], x[6], x[7]);
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int d = d0 + i;
-                    if (d < half) x[i] = x[i] * cs[t][d] - rows[warp][d + half] * sn[t][d];
-                    else if (d < 2 * half) x[i] = x[i] * cs[t][d - half] + rows[warp][d - half] * sn[t][d - half];
+                    if (d < half) x[i] = x[i] * cs[t][at_pair(d)] - rows[warp][d + half] * sn[t][at_pair(d)];
+                    else if (d < 2 * half) x[i] = x[i] * cs[t][at_pair(d - half)] + rows[warp][d - half] * sn[t][at_pair(d - half)];
                 }
             }
         }
@@ -140,11 +148,12 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
-    // Few tokens: one a CTA, as many CTAs as there can be.  Many: four, whose loads are all in flight at once.
+    // Few tokens: one a CTA, as many CTAs as there can be.  Many: two, whose loads are both in flight (8 x 256
+    // tokens of 4 groups, 42 MB: 17.3 us with one, 14.8 with two at 8 CTAs an SM, 15.7 with four at 5).
     const int64_t tokens = (int64_t)a.B * a.n;
     const bool many = tokens * a.G >= 4096;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((many ? (tokens + 3) / 4 : tokens) * a.G), 1, 1);
+    cfg.gridDim = dim3((unsigned)((many ? (tokens + 1) / 2 : tokens) * a.G), 1, 1);
     cfg.blockDim = dim3(kRopeThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -152,7 +161,7 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<4>, a) : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<1>, a);
+    return many ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<2>, a) : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<1>, a);
 }
 
 }  // namespace rma
