@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
                     cf[x] = s.rk[8 * p + x] * ex2((rh - Gh[8 * p + x]) + (rl - Gl[8 * p + x]));
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
                     const int i = (gt >> 3) + 16 * k;
                     if ((i >> 3) == p) continue;   // the diagonal's
@@ -577,27 +577,24 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                 }
                 const int e = scale_exponent(tmax, 8);
                 const float sc = pow2(e);
-                float sum[4];
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 4; ++k) {
                     const int i = (gt >> 3) + 16 * k;
                     const float4 t0 = *reinterpret_cast<const float4*>(&T[i][8 * p]), t1 = *reinterpret_cast<const float4*>(&T[i][8 * p + 4]);
                     const float v[8] = {t0.x * b0.x, t0.y * b0.y, t0.z * b0.z, t0.w * b0.w, t1.x * b1.x, t1.y * b1.y, t1.z * b1.z, t1.w * b1.w};
-                    sum[k] = 0.f;
+                    float sum = 0.f;
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        sum[k] += fabsf(v[2 * x]) + fabsf(v[2 * x + 1]);
+                        sum += fabsf(v[2 * x]) + fabsf(v[2 * x + 1]);
                         split2(v[2 * x] * sc, v[2 * x + 1] * sc, hi[x], lo[x]);
                     }
                     *reinterpret_cast<uint4*>(out + piece_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4*>(out + kOffTLo + piece_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                    if (p == 0) s.tsum[grp][i] = sum;
                 }
-#pragma unroll
-                for (int o = 4; o > 0; o >>= 1)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
-                if (p < 4) s.tsum[grp][(gt >> 3) + 16 * p] = p == 0 ? sum[0] : p == 1 ? sum[1] : p == 2 ? sum[2] : sum[3];
                 ptx::named_bar_sync(bar, 128);
                 if (gw == 0) {
                     float bw = 0.f, bt = 0.f, bs = 0.f;

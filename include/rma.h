@@ -450,12 +450,19 @@ RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qk
  * sequence is in, which then stands after its last token.
  *   qkv      bf16 [batch][n_tok][C];  a, b  bf16 [batch][n_tok][n_v_heads],
  *            consecutive tokens ab_stride elements apart
- *   lens     i32  [batch] or NULL, as in rma_gdn_conv
+ *   lens     i32  [batch] or NULL, as in rma_gdn_conv: rows past them have no effect, whatever they
+ *            hold, and their outputs are not written
  *   out      bf16 [batch][n_tok][n_v_heads][128]   (written; must not overlap an input)
  *   ws       workspace of rma_gdn_workspace_bytes(st, n_tok) bytes
  * n_tok >= 1 and batch * n_tok <= 2^24.  qkv of the tokens inside the lengths
  * must be finite: a NaN or infinity there spoils its sequence's outputs from up
- * to 63 tokens before it on, and the state. */
+ * to 63 tokens before it on, and the state.
+ * Blocks of 13 tokens and more (9 and more where 4 batch * n_v_heads exceeds
+ * the SM count) run in chunks of 64, two launches on the stream, shorter ones
+ * token by token.  The chunks keep the
+ * state to about 2^-21 of its largest values, as FP32 sums do; the outputs,
+ * before their rounding to BF16, to 2^-10 of their terms.  After
+ * RMA_STATUS_TIMEOUT the delta state and outputs of the call are not valid. */
 RMA_API int rma_gdn_prefill(rma_gdn_state* st, int layer, int n_tok, const uint16_t* qkv,
                     const uint16_t* a, const uint16_t* b, int64_t ab_stride,
                     const float* a_log, const float* dt_bias, const int32_t* lens, uint16_t* out,

@@ -297,6 +297,24 @@ def test_block_of_more_heads_than_multiprocessors():
         assert torch.equal(again[b], out[b]) and torch.equal(few.delta[0, 0], st.delta[0, b])
 
 
+@pytest.mark.parametrize("batch,hk,hv,n,lens", [(1, 1, 2, 1700, None), (3, 2, 4, 1601, [1601, 500, 40]), (2, 2, 20, 1540, [0, 1537])])
+def test_long_blocks_of_few_heads(batch, hk, hv, n, lens):
+    """Prompts of many chunks, back to back on one workspace; sequences end in any chunk."""
+    rma, st, d, x = delta_case(batch, n, hk, hv, seed=73 + batch)
+    out = torch.full((batch, n, hv, 128), 7.0, dtype=BF, device="cuda")
+    ws = st.workspace(n)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    first = None
+    for _ in range(3):
+        st.delta[0].copy_(d["state"])
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, ws, lens=ln)
+        if first is None:
+            first = (out.clone(), st.delta.clone())
+        assert torch.equal(out, first[0]) and torch.equal(st.delta, first[1])
+    past = delta_check(out, st.delta[0], x, hk, lens=lens)
+    assert (f64(out)[past] == 7.0).all() and rma.gdn_get_status(st) == 0
+
+
 def test_lengths_out_of_range_are_clamped_and_reported():
     rma, st, d, x = delta_case(2, 70, 1, 2, seed=80)
     out = torch.full((2, 70, 2, 128), 7.0, dtype=BF, device="cuda")
