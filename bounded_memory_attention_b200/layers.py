@@ -8,7 +8,6 @@ on another stream than its own is in flight must be kept alive by the caller.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -17,49 +16,47 @@ import torch
 from . import RmaError, _check, _GdnConfig, _GdnLayout, lib  # noqa: F401
 
 _BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
-_HERE = contextlib.nullcontext()
 _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(index: int):
-    """A context in which device `index` is the current one."""
-    return _HERE if _current_device() == index else torch.cuda.device(index)
+def _call(function, name: str, index: int, stream, *args) -> None:
+    """`function(*args, stream)` with device `index` current; its error raised."""
+    if _current_device() == index:
+        code = function(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            code = function(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if code != 0:
+        raise RmaError(code, name)
 
 
-def _stream(stream, index: int) -> int:
-    return _raw_stream(index) if stream is None else stream.cuda_stream
-
-
-def _wrong(t, dtype, name: str, index: int):
+def _wrong(t, dtype, name: str, index: int, otherwise: str):
     """What is wrong with `t` as a tensor of `dtype` on CUDA device `index`."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         return TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
         return TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return ValueError(f"{name} is on {t.device}, the state on device {index}")
+    if t.get_device() != index:
+        return ValueError(f"{name} is on {t.device}, the state on device {index}")
+    return ValueError(otherwise)
 
 
 def _dense(t, dtype, numel: int, name: str, index: int) -> int:
     """The address of a contiguous tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or t.get_device() != index:
-        raise _wrong(t, dtype, name, index)
-    if t.numel() != numel:
-        raise ValueError(f"{name} has {t.numel()} elements, expected {numel}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.numel() == numel
+            and t.is_contiguous()):
+        return t.data_ptr()
+    raise _wrong(t, dtype, name, index, f"{name} must be contiguous, of {numel} elements: got {list(getattr(t, 'shape', []))}")
 
 
 def _rows(t, dtype, batch: int, n: int, inner: tuple, name: str, index: int):
     """(address, elements from one token to the next) of a [batch, n, *inner] tensor (or
     [batch, *inner] for n == 1) whose tokens are contiguous rows, evenly spaced over the batch too."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or t.get_device() != index:
-        raise _wrong(t, dtype, name, index)
     row = inner[0] if len(inner) == 1 else inner[0] * inner[1]
-    shape = t.shape
-    if shape != (batch, n, *inner) and not (n == 1 and shape == (batch, *inner)):
-        raise ValueError(f"{name} has shape {list(shape)}, expected {[batch, n, *inner]}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and (t.shape == (batch, n, *inner) or n == 1 and t.shape == (batch, *inner))):
+        raise _wrong(t, dtype, name, index, f"{name} must be {[batch, n, *inner]}: got {list(getattr(t, 'shape', []))}")
     if t.is_contiguous():
         return t.data_ptr(), row
     strides = t.stride()
@@ -96,7 +93,8 @@ def qk_norm_rope(state, layer: int, q, k, w_q, w_k, inv_freq, q_out, k_out, posi
     for the places that the layer's counters give the next tokens."""
     c = state.cfg
     device = state.buffer.get_device()
-    B, G, HQ, D = c.batch, c.n_groups, c.n_q_heads, c.head_dim
+    B, G, D = c.batch, c.n_groups, c.head_dim
+    HQ = G * c.q_per_group
     n = _tokens(q, B, 4, "q")
     qp, qs = _rows(q, _BF16, B, n, (HQ, D), "q", device)
     kp, ks = _rows(k, _BF16, B, n, (G, D), "k", device)
@@ -105,9 +103,7 @@ def qk_norm_rope(state, layer: int, q, k, w_q, w_k, inv_freq, q_out, k_out, posi
             _dense(inv_freq, _F64, pairs, "inv_freq", device) if pairs else None, 2 * pairs, 1 if interleaved else 0,
             None if positions is None else _dense(positions, _I32, B * n, "positions", device),
             _dense(q_out, _BF16, B * n * HQ * D, "q_out", device), _dense(k_out, _BF16, B * n * G * D, "k_out", device))
-    with _on(device):
-        _check(lib.rma_qk_norm_rope(state.handle, int(layer), n, qp, qs, kp, ks, *args, _stream(stream, device)),
-               "rma_qk_norm_rope")
+    _call(lib.rma_qk_norm_rope, "rma_qk_norm_rope", device, stream, state._h, layer, n, qp, qs, kp, ks, *args)
     return q_out, k_out
 
 
@@ -166,8 +162,9 @@ class GdnState:
         c = cfg._c()
         lay = _GdnLayout()
         device = self.buffer.get_device()
-        with _on(device):
-            _check(lib.rma_gdn_state_alloc(ctypes.byref(c), self.buffer.data_ptr(), n, _stream(stream, device),
+        with torch.cuda.device(device):
+            _check(lib.rma_gdn_state_alloc(ctypes.byref(c), self.buffer.data_ptr(), n,
+                                           _raw_stream(device) if stream is None else stream.cuda_stream,
                                            ctypes.byref(self._h)), "rma_gdn_state_alloc")
         _check(lib.rma_gdn_state_layout(self._h, ctypes.byref(lay)), "rma_gdn_state_layout")
         self.layout = {f: int(getattr(lay, f)) for f, _ in _GdnLayout._fields_}
@@ -226,9 +223,8 @@ def gdn_conv(state: GdnState, layer: int, x, w, out, bias=None, lens=None, strea
     wp = _dense(w, _F32, C * c.conv_width, "w", device)
     bp = None if bias is None else _dense(bias, _F32, C, "bias", device)
     op = _dense(out, _BF16, B * n * C, "out", device)
-    with _on(device):
-        _check(lib.rma_gdn_conv(state.handle, int(layer), n, xp, xs, wp, bp, _lens(lens, B, device), op,
-                                _stream(stream, device)), "rma_gdn_conv")
+    _call(lib.rma_gdn_conv, "rma_gdn_conv", device, stream, state._h, layer, n, xp, xs, wp, bp,
+          _lens(lens, B, device), op)
     return out
 
 
@@ -250,9 +246,7 @@ def gdn_decode_step(state: GdnState, layer: int, qkv, a, b, a_log, dt_bias, out,
     args = (_dense(qkv, _BF16, B * c.channels, "qkv", device), ap, bp, stride,
             _dense(a_log, _F32, HV, "a_log", device), _dense(dt_bias, _F32, HV, "dt_bias", device),
             _dense(out, _BF16, B * HV * c.head_dim, "out", device))
-    with _on(device):
-        _check(lib.rma_gdn_decode_step(state.handle, int(layer), *args, _stream(stream, device)),
-               "rma_gdn_decode_step")
+    _call(lib.rma_gdn_decode_step, "rma_gdn_decode_step", device, stream, state._h, layer, *args)
     return out
 
 
@@ -268,8 +262,7 @@ def gdn_prefill(state: GdnState, layer: int, qkv, a, b, a_log, dt_bias, out, ws,
             _dense(a_log, _F32, HV, "a_log", device), _dense(dt_bias, _F32, HV, "dt_bias", device),
             _lens(lens, B, device), _dense(out, _BF16, B * n * HV * c.head_dim, "out", device),
             _dense(ws, torch.uint8, ws.numel(), "ws", device), ws.numel())
-    with _on(device):
-        _check(lib.rma_gdn_prefill(state.handle, int(layer), n, *args, _stream(stream, device)), "rma_gdn_prefill")
+    _call(lib.rma_gdn_prefill, "rma_gdn_prefill", device, stream, state._h, layer, n, *args)
     return out
 
 
@@ -277,7 +270,7 @@ def gdn_get_status(state: GdnState, stream=None) -> int:
     """Wait for the stream, then read and clear the GDN state's status word (STATUS_* bits)."""
     flags = ctypes.c_uint32()
     device = state.buffer.get_device()
-    with _on(device):
-        _check(lib.rma_gdn_get_status(state.handle, _stream(stream, device), ctypes.byref(flags)),
-               "rma_gdn_get_status")
+    with torch.cuda.device(device):
+        _check(lib.rma_gdn_get_status(state._h, _raw_stream(device) if stream is None else stream.cuda_stream,
+                                      ctypes.byref(flags)), "rma_gdn_get_status")
     return int(flags.value)

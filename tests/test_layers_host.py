@@ -91,6 +91,6 @@ def test_token_strides_of_views():
         with pytest.raises(ValueError):
             bad()
     with pytest.raises(TypeError):
-        layers._rows(wide, torch.bfloat16, 2, 3, (640,), "x", -1)
+        layers._rows(wide, torch.bfloat16, 2, 3, (640,), "x", 0)   # on the CPU
     with pytest.raises(TypeError):
         rows(wide.float(), 2, 3, (640,))
