@@ -11,6 +11,13 @@
 // and its reduction to a fraction of a turn are in FP64; the fraction's sine and cosine then need FP32
 // only.  Partners in another lane come by shuffles, or through the warp's row of shared memory where a lane's
 // eight values do not have one side (rotary_dim / 2 not a multiple of 8).
+//
+// Measured on one B200, 4 groups: 1.9 us for one token, 5.1 us for 512 sequences of one token (64 values
+// rotated), 14.8 us for 8 x 256 tokens with all 256 rotated (42 MB, 2.8 TB/s).  The last is 3.5 waves of short
+// CTAs that issue in 78% of the cycles, about a third of it for the angles, which every group computes for
+// itself (its counter is its own).  Two FP32 values an instruction and one table for four groups gave 14.0 us
+// there but 5.5 us for the 512.
+
 #include <cuda_bf16.h>
 
 #include "rma_internal.cuh"

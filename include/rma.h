@@ -322,7 +322,9 @@ RMA_API int rma_get_status(rma_state* st, void* stream, uint32_t* flags);
  * caller-owned device memory, asynchronous calls that can be captured into a
  * graph, argument errors found on the host, device conditions in a status
  * word.  The calling thread's current device must be the one the state was
- * laid out on (RMA_ERR_INVALID_ARG otherwise).
+ * laid out on (RMA_ERR_INVALID_ARG otherwise).  Calls on one layer of a state
+ * must follow one another: on one stream, or on streams that the caller orders
+ * by events; calls on different layers may overlap.
  * ====================================================================== */
 
 /* Per-head RMS norm of queries and keys, then the position rotation, in one
@@ -459,10 +461,10 @@ RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qk
  * to 63 tokens before it on, and the state.
  * Blocks of 13 tokens and more (9 and more where 4 batch * n_v_heads exceeds
  * the SM count) run in chunks of 64, two launches on the stream, shorter ones
- * token by token.  The chunks keep the
- * state to about 2^-21 of its largest values, as FP32 sums do; the outputs,
- * before their rounding to BF16, to 2^-10 of their terms.  After
- * RMA_STATUS_TIMEOUT the delta state and outputs of the call are not valid. */
+ * token by token.  The chunks keep the state to about 2^-21 of its largest
+ * values, as FP32 sums do; the outputs, before their rounding to BF16, to
+ * 2^-10 of their terms.  After RMA_STATUS_TIMEOUT the delta state and outputs
+ * of the call are not valid. */
 RMA_API int rma_gdn_prefill(rma_gdn_state* st, int layer, int n_tok, const uint16_t* qkv,
                     const uint16_t* a, const uint16_t* b, int64_t ab_stride,
                     const float* a_log, const float* dt_bias, const int32_t* lens, uint16_t* out,
