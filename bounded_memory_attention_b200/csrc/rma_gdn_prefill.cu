@@ -7,7 +7,7 @@
 //   S1 = e^{G_C} S0 + sum_j e^{G_C - G_j} k_j u_j^T.
 // With T = (1 + A)^-1 diag(beta), U = T (V - diag(e^G) K S0).
 //
-// Two launches.
+// Two launches, or for few heads both in one (gdn_joint_kernel).
 //
 // 1. gdn_prep_kernel, a CTA per (chunk, sequence, key head): everything that does not depend on the
 //    state.  Norms of q and k; K K^T and Q K^T once per key head; per value head of it the decays, T
@@ -120,10 +120,12 @@ constexpr int kRowTop = 4;         // the largest value of a scaled row of K or 
 constexpr int kHeadsAtOnce = 4;    // value heads whose gates are computed together, one per warp
 constexpr int kLd = kC + 4;        // row of a matrix that the tensor cores' fragments are read from
 
-// Measured on one B200: 81 us for 8,192 tokens of 16 key and 32 value heads, 2,048 CTAs.  It issues in half of
+// Measured on one B200: 80 us for 8,192 tokens of 16 key and 32 value heads, 2,048 CTAs.  It issues in half of
 // the cycles, 25,000 warp instructions a CTA; what stalls it are the group's barriers between the short phases
 // (24 warps an SM, which registers and shared memory both limit) and shared memory, half of its wavefronts.
-// K K^T and Q K^T by tcgen05 instead of mma.sync took the same time: the products are a small part.
+// K K^T and Q K^T by tcgen05 instead of mma.sync took the same time: the products are a small part.  So did fewer
+// instructions (two FP32 values each, sums of |K| from the norms), the inverse over four warps instead of two, and
+// the gates off the critical path.
 //
 // Two groups of four warps, each with a value head of its own at a time.
 struct __align__(1024) PrepSmem {
@@ -285,15 +287,18 @@ __device__ __forceinline__ void invert(float (*T)[kLd], int warp, int lane, int 
     ptx::named_bar_sync(bar, 128);
 }
 
-__global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
-    extern __shared__ uint8_t smem_raw[];
-    PrepSmem& s = *reinterpret_cast<PrepSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = warp_index(), lane = tid & 31;
-    const int kh = blockIdx.x % a.HK;
-    const int b = (blockIdx.x / a.HK) % a.B;
-    const int c = blockIdx.x / a.HK / a.B;
-    grid_dep_wait();
-    grid_dep_launch();
+// Item `item` (chunk, sequence, key head) by 256 threads, all of a CTA's or a slot's, `tid` and `warp` among them.
+// Named barriers: kAlone 1 and 2, otherwise three from bar0 on.
+template <bool kAlone>
+__device__ __forceinline__ void prep_item(const DeltaArgs& a, PrepSmem& s, int NC, uint32_t item, int tid, int warp, int bar0) {
+    const int lane = tid & 31;
+    auto sync = [&] {
+        if constexpr (kAlone) __syncthreads();
+        else ptx::named_bar_sync(bar0, kPrepThreads);
+    };
+    const int kh = item % (uint32_t)a.HK;
+    const int b = (item / (uint32_t)a.HK) % (uint32_t)a.B;
+    const int c = item / (uint32_t)a.HK / (uint32_t)a.B;
     const int len = seq_len(a.lens, b, a.n, a.status, c == 0 && kh == 0 && tid == 0);
     const int t0 = c * kC;
     const int valid = min(len - t0, kC);
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
             }
         }
     }
-    __syncthreads();
+    sync();
 
     // rows 16 rb .. + 15 of K K^T (warps 0-3) or Q K^T (warps 4-7), up to the diagonal block
     {
@@ -460,7 +465,7 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
                 }
             }
         }
-        __syncthreads();   // the images have been read
+        sync();   // the images have been read
         float* prod = &s.prod[m][0][0];
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
@@ -482,14 +487,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
     }
     const int ep = scale_exponent(pmax, 8);
     const float p_scale = pow2(ep);
-    __syncthreads();
+    sync();
 
-    const int grp = warp >> 2, gt = tid & 127, gw = warp & 3, bar = 1 + grp;
+    const int grp = warp >> 2, gt = tid & 127, gw = warp & 3, bar = (kAlone ? 1 : bar0 + 1) + grp;
     for (int r0 = 0; r0 < R; r0 += kHeadsAtOnce) {
         if (r0 > 0) {
-            __syncthreads();
+            sync();
             head_gates(r0);
-            __syncthreads();
+            sync();
         }
         for (int r = r0 + grp; r < min(r0 + kHeadsAtOnce, R); r += 2) {
             const float *Gh = s.Gh[r - r0], *Gl = s.Gl[r - r0], *beta = s.beta[r - r0];
@@ -633,6 +638,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
     }
 }
 
+__global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_constant__ DeltaArgs a, int NC) {
+    extern __shared__ uint8_t smem_raw[];
+    PrepSmem& s = *reinterpret_cast<PrepSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    grid_dep_wait();
+    grid_dep_launch();
+    prep_item<true>(a, s, NC, blockIdx.x, threadIdx.x, warp_index(), 0);
+}
+
 // ---------------------------------------------------------------------------
 // launch 2
 //
@@ -749,8 +762,32 @@ __device__ __forceinline__ void lds4(const float* p, f2& a, f2& b) {
     b = v.y;
 }
 
-__global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_constant__ DeltaArgs a,
-                                                                   const __grid_constant__ ScanMaps maps, int NC) {
+// Wait, bounded as the waits on barriers are, until another CTA has set the flag.  By a whole warp, with one verdict.
+__device__ __forceinline__ bool item_ready(const uint32_t* flag, volatile int* abort, uint32_t* status) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) {
+        const long long t0 = clock64();
+        uint32_t v;
+        while (true) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(v) : "l"(flag) : "memory");
+            if (v != 0) break;
+            if (*abort || clock64() - t0 > ptx::kWaitLimitCycles) {
+                *abort = 1;
+                atomicOr(status, (unsigned)RMA_STATUS_TIMEOUT);
+                ok = false;
+                break;
+            }
+            __nanosleep(64);
+        }
+        asm volatile("fence.proxy.async;\n" ::: "memory");   // the loads that follow are another proxy's
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
+// Head `index` of `heads`, in the order (sequence, value head).  `ready`: NULL where the first launch is complete;
+// otherwise a flag per item of it, which the same launch's other CTAs set.
+__device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& maps, int NC, int index, int heads,
+                                          const uint32_t* ready) {
     extern __shared__ uint8_t smem_raw[];
     // the same place as a shared-memory address and as a pointer
     const uint32_t smem_base = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -763,11 +800,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     int8_t* exps = reinterpret_cast<int8_t*>(smem + kScanExp);
     // More heads than multiprocessors and lengths that differ: the longest sequences' CTAs first, so that what
     // is dealt out last is short.
-    const int h = blockIdx.x % a.HV, kh = h / (a.HV / a.HK);
-    int b = blockIdx.x / a.HV;
-    const bool ordered = a.lens && a.B > 1 && a.B <= kMaxOrder && (int)gridDim.x > a.sm_count;
+    const int h = index % a.HV, kh = h / (a.HV / a.HK);
+    int b = index / a.HV;
+    const bool ordered = a.lens && a.B > 1 && a.B <= kMaxOrder && heads > a.sm_count;
     if (!ordered && tid == 0)   // the state towards L2, before anything is waited for
-        prefetch_l2(a.state + (int64_t)blockIdx.x * kGdnDim * kGdnDim, kGdnDim * kGdnDim * 4);
+        prefetch_l2(a.state + (int64_t)index * kGdnDim * kGdnDim, kGdnDim * kGdnDim * 4);
     grid_dep_wait();
     grid_dep_launch();
     if (ordered) {
@@ -823,6 +860,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
                 if (c >= kStages && !ptx::mbar_wait_warp(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag, a.status)) break;
                 // the state and the first chunk come first: they are what the start waits for
                 if (c == 1 && !ptx::mbar_wait_warp(&bars[kbS], 0, abort_flag, a.status)) break;
+                if (ready && !item_ready(ready + ((int64_t)c * a.B + b) * a.HK + kh, abort_flag, a.status)) break;
                 issued = c + 1;
                 uint8_t* stage = smem + st * kStageBytes;
                 if (lane == 0) {
@@ -1196,6 +1234,46 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
     if (warp == kWarpMma) ptx::tmem_dealloc1(tmem, kTmCols);
 }
 
+__global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_constant__ DeltaArgs a,
+                                                                   const __grid_constant__ ScanMaps maps, int NC) {
+    scan_head(a, maps, NC, blockIdx.x, gridDim.x, nullptr);
+}
+
+// ---------------------------------------------------------------------------
+// Both in one launch, for few heads and many chunks: a CTA an SM, the first ones the heads of launch 2, the others two
+// items at a time of launch 1, chunk by chunk.  A finished item sets its flag, and a head's loads wait for it.  The
+// launch is cooperative, so that all CTAs are there, and those that are waited for do not wait themselves.
+//
+// Measured on one B200, 16 key and 32 value heads: 333 us for 8,192 tokens (386 in two launches), 103 (108) for 2,048,
+// 64 (62) for 1,024; two sequences of 4,096 tokens 203 (242).
+// ---------------------------------------------------------------------------
+constexpr int kPrepSlot = (sizeof(PrepSmem) + 1023) / 1024 * 1024;
+static_assert(2 * kPrepThreads == kScanThreads && 2 * kPrepSlot + 1024 <= kScanSmem, "two items in a CTA of the scan's size");
+
+__global__ void __launch_bounds__(kScanThreads, 1) gdn_joint_kernel(const __grid_constant__ DeltaArgs a, const __grid_constant__ ScanMaps maps,
+                                                                    int NC, uint32_t* ready) {
+    extern __shared__ uint8_t smem_raw[];
+    const int heads = a.B * a.HV, workers = gridDim.x - heads;
+    grid_dep_launch();
+    // The heads first: the first CTAs of a launch are placed in pairs on neighbours, far from the other pairs, and take
+    // 4,200 cycles a chunk (4,500 beside the others' work).  On every other SM they took up to 5,700.
+    if ((int)blockIdx.x < heads) {
+        scan_head(a, maps, NC, blockIdx.x, heads, ready);
+        return;
+    }
+    const int index = blockIdx.x - heads;
+    const int w = warp_index(), slot = w >> 3, tid = threadIdx.x & (kPrepThreads - 1);
+    uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    PrepSmem& s = *reinterpret_cast<PrepSmem*>(base + slot * kPrepSlot);
+    const int items = NC * a.B * a.HK;
+    const int bar0 = 1 + 3 * slot;
+    for (int item = index + slot * workers; item < items; item += 2 * workers) {
+        prep_item<false>(a, s, NC, item, tid, w & 7, bar0);
+        ptx::named_bar_sync(bar0, kPrepThreads);   // also before the next item's shared memory
+        if (tid == 0) asm volatile("st.release.gpu.global.u32 [%0], %1;\n" ::"l"(ready + item), "r"(1u) : "memory");
+    }
+}
+
 // A 2-D BF16 tensor of `rows` rows of `cols` values, boxes of bc columns x 64 rows.
 bool make_map2(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t bc, CUtensorMapSwizzle swizzle) {
     TensorMapEncodeFn fn = tensor_map_encode();
@@ -1211,11 +1289,22 @@ bool make_map2(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, u
 
 }  // namespace
 
+// the operands, then a flag per item
+static size_t operand_bytes(size_t NC, size_t B, size_t HK, size_t HV) {
+    return (NC * B * (HK * kKQBytes + HV * kTPBytes) + 255) / 256 * 256;
+}
+
 size_t gdn_prefill_workspace_bytes(const rma_gdn_config& c, int n) {
     if (n < kGdnChunkedFrom) return 256;
     const size_t NC = (n + kC - 1) / kC;
-    const size_t bytes = NC * c.batch * ((size_t)c.n_k_heads * kKQBytes + (size_t)c.n_v_heads * kTPBytes);
-    return (bytes + 255) / 256 * 256;
+    return operand_bytes(NC, c.batch, c.n_k_heads, c.n_v_heads) + (NC * c.batch * c.n_k_heads * 4 + 255) / 256 * 256;
+}
+
+// Heads on at most half of the multiprocessors, 32 chunks or more, and the others keep ahead of the heads: an item
+// with two value heads takes 12 us, two items at a time a CTA, a chunk of the scan 2.3 us.
+static bool in_one_launch(const DeltaArgs& a, int NC) {
+    const int heads = a.B * a.HV, rest = a.sm_count - heads;
+    return NC >= 32 && rest >= heads && 5ll * a.B * a.HK * ((a.HV / a.HK + 1) / 2) <= 2 * rest;
 }
 
 cudaError_t launch_gdn_prefill(const DeltaArgs& a, cudaStream_t stream) {
@@ -1235,6 +1324,20 @@ cudaError_t launch_gdn_prefill(const DeltaArgs& a, cudaStream_t stream) {
     if (!make_map2(&maps.v, a.qkv, a.C, rows, kGdnDim, CU_TENSOR_MAP_SWIZZLE_NONE) ||
         !make_map2(&maps.out, a.out, (uint64_t)a.HV * kGdnDim, rows, 64, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
+    if (in_one_launch(a, NC)) {
+        static SmemLimit joint_limit(reinterpret_cast<const void*>(gdn_joint_kernel));
+        e = joint_limit.ensure(kScanSmem);
+        if (e != cudaSuccess) return e;
+        uint32_t* ready = reinterpret_cast<uint32_t*>(a.ws + operand_bytes(NC, a.B, a.HK, a.HV));
+        e = cudaMemsetAsync(ready, 0, grid * 4, stream);
+        if (e != cudaSuccess) return e;
+        PdlLaunch l((unsigned)a.sm_count, kScanThreads, kScanSmem, stream);
+        l.attr[0].id = cudaLaunchAttributeCooperative;
+        l.attr[0].val.cooperative = 1;
+        e = cudaLaunchKernelEx(&l.cfg, gdn_joint_kernel, a, maps, NC, ready);
+        if (e != cudaErrorCooperativeLaunchTooLarge) return e;
+        cudaGetLastError();   // a context that has not all of the device's multiprocessors
+    }
     PdlLaunch prep((unsigned)grid, kPrepThreads, prep_smem, stream);
     e = cudaLaunchKernelEx(&prep.cfg, gdn_prep_kernel, a, NC);
     if (e != cudaSuccess) return e;

@@ -460,8 +460,10 @@ RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qk
  * must be finite: a NaN or infinity there spoils its sequence's outputs from up
  * to 63 tokens before it on, and the state.
  * Blocks of 13 tokens and more (9 and more where 4 batch * n_v_heads exceeds
- * the SM count) run in chunks of 64, two launches on the stream, shorter ones
- * token by token.  The chunks keep the state to about 2^-21 of its largest
+ * the SM count) run in chunks of 64, two launches on the stream (for few heads
+ * and 32 chunks or more a memset and one cooperative launch of a block on every
+ * SM, which waits until all SMs are free), shorter ones token by token.  The
+ * chunks keep the state to about 2^-21 of its largest
  * values, as FP32 sums do; the outputs, before their rounding to BF16, to
  * 2^-10 of their terms.  After RMA_STATUS_TIMEOUT the delta state and outputs
  * of the call are not valid. */

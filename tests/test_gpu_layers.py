@@ -315,6 +315,75 @@ def test_long_blocks_of_few_heads(batch, hk, hv, n, lens):
     assert (f64(out)[past] == 7.0).all() and rma.gdn_get_status(st) == 0
 
 
+@pytest.mark.parametrize("batch,hk,hv,n,lens", [(1, 1, 2, 2049, None), (3, 2, 4, 2100, [2100, 0, 1990]), (2, 3, 9, 2050, [777, 2050]),
+                                                (1, 5, 5, 1985, None)])
+def test_blocks_long_enough_for_one_launch(batch, hk, hv, n, lens):
+    """32 chunks and more of few heads go in one launch: against the oracle, whatever the workspace held (its flags
+    among it), with NaN in the padding, and the same bits every time."""
+    rma, st, d, x = delta_case(batch, n, hk, hv, seed=173 + batch)
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    if lens is not None:
+        for b, m in enumerate(lens):
+            d["qkv"][b, m:] = float("nan")
+    ws = st.workspace(n)
+    first = None
+    for fill in (1, 255, 0, None):
+        out = torch.full((batch, n, hv, 128), 7.0, dtype=BF, device="cuda")
+        if fill is not None:
+            ws.fill_(fill)
+        st.delta[0].copy_(d["state"])
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, ws, lens=ln)
+        if first is None:
+            first = (out.clone(), st.delta.clone())
+        assert torch.equal(out, first[0]) and torch.equal(st.delta, first[1])
+    past = delta_check(out, st.delta[0], x, hk, lens=lens)
+    assert (f64(out)[past] == 7.0).all() and rma.gdn_get_status(st) == 0
+
+
+def test_long_blocks_at_once_and_replayed():
+    """Two long blocks of two states on two streams at once, then both replayed from graphs at once, between calls of
+    the other kinds: the bits of the calls alone."""
+    rma = lib()
+    sides = []
+    for side in range(2):
+        rma, st, d, x = delta_case(1, 2048, 2, 4, seed=180 + side)
+        w = si.f32_normal((st.cfg.channels, 4), 182 + side, std=0.5).cuda()
+        ws, out = st.workspace(2048), torch.empty(1, 2048, 4, 128, dtype=BF, device="cuda")
+        y, one = torch.empty_like(d["qkv"]), torch.empty(1, 4, 128, dtype=BF, device="cuda")
+
+        def call(st=st, d=d, w=w, ws=ws, out=out, y=y, one=one):
+            rma.gdn_conv(st, 0, d["qkv"], w, y)
+            rma.gdn_prefill(st, 0, y, d["a"], d["b"], d["a_log"], d["dt_bias"], out, ws)
+            rma.gdn_decode_step(st, 0, y[:, 99].contiguous(), d["a"][:, 99], d["b"][:, 99], d["a_log"], d["dt_bias"], one)
+
+        call()
+        torch.cuda.synchronize()
+        stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        sides.append((st, d, out, one, (out.clone(), one.clone(), st.buffer.clone()), call, stream, graph))
+
+    def at_once(run):
+        for st, d, out, *_ in sides:
+            st.conv.zero_()
+            st.delta[0].copy_(d["state"])
+            out.fill_(3.0)
+        torch.cuda.synchronize()
+        for side in sides:
+            with torch.cuda.stream(side[6]):
+                run(side)
+        torch.cuda.synchronize()
+        for st, d, out, one, want, *_ in sides:
+            assert torch.equal(out, want[0]) and torch.equal(one, want[1]) and torch.equal(st.buffer, want[2])
+            assert rma.gdn_get_status(st) == 0
+
+    for _ in range(3):
+        at_once(lambda side: side[5]())
+    for side in sides:
+        with torch.cuda.graph(side[7], stream=side[6]):
+            side[5]()
+    for _ in range(3):
+        at_once(lambda side: side[7].replay())
+
+
 def test_lengths_out_of_range_are_clamped_and_reported():
     rma, st, d, x = delta_case(2, 70, 1, 2, seed=80)
     out = torch.full((2, 70, 2, 128), 7.0, dtype=BF, device="cuda")
