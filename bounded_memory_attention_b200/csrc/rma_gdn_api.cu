@@ -37,6 +37,10 @@ uint64_t span(int64_t rows, int64_t stride, int64_t cols, int64_t size) {
 GdnState* as_gdn(rma_gdn_state* p) { return reinterpret_cast<GdnState*>(p); }
 const GdnState* as_gdn(const rma_gdn_state* p) { return reinterpret_cast<const GdnState*>(p); }
 
+bool in_state(const GdnState* s, const void* p, uint64_t bytes) {
+    return overlap(p, bytes, s->base, s->lay.total_bytes);
+}
+
 int channels(const rma_gdn_config& c) { return (2 * c.n_k_heads + c.n_v_heads) * c.head_dim; }
 
 int check_gdn_config(const rma_gdn_config* c) {
@@ -112,9 +116,13 @@ int delta_args(const GdnState* s, int layer, int n, const uint16_t* qkv, const u
     const int C = channels(c);
     const uint64_t ob = span(rows, c.n_v_heads * kGdnDim, c.n_v_heads * kGdnDim, 2);
     const uint64_t ab = span(rows, ab_stride, c.n_v_heads, 2);
-    if (overlap(out, ob, qkv, span(rows, C, C, 2)) || overlap(out, ob, a, ab) || overlap(out, ob, b, ab) ||
-        overlap(out, ob, a_log, 4ull * c.n_v_heads) || overlap(out, ob, dt_bias, 4ull * c.n_v_heads) ||
-        overlap(out, ob, lens, 4ull * c.batch) || overlap(out, ob, s->base, s->lay.total_bytes))
+    const uint64_t xb = span(rows, C, C, 2), hb = 4ull * c.n_v_heads;
+    if (in_state(s, qkv, xb) || in_state(s, a, ab) || in_state(s, b, ab) || in_state(s, a_log, hb) ||
+        in_state(s, dt_bias, hb) || in_state(s, lens, 4ull * c.batch))
+        return api_fail(RMA_ERR_INVALID_ARG, "an input overlaps the state");
+    if (overlap(out, ob, qkv, xb) || overlap(out, ob, a, ab) || overlap(out, ob, b, ab) ||
+        overlap(out, ob, a_log, hb) || overlap(out, ob, dt_bias, hb) || overlap(out, ob, lens, 4ull * c.batch) ||
+        in_state(s, out, ob))
         return api_fail(RMA_ERR_INVALID_ARG, "out overlaps an input or the state");
     const uint64_t l = (uint64_t)layer;
     d.qkv = qkv;
@@ -280,10 +288,11 @@ int rma_gdn_conv(rma_gdn_state* st, int layer, int n_tok, const uint16_t* x, int
     if (x_stride < C || x_stride % 8 != 0 || x_stride > (1ll << 32))
         return api_fail(RMA_ERR_INVALID_ARG, "x_stride must be a multiple of 8, at least the channels (and <= 2^32)");
     const int64_t rows = (int64_t)c.batch * n_tok;
-    const uint64_t ob = span(rows, C, C, 2);
-    if (overlap(out, ob, x, span(rows, x_stride, C, 2)) || overlap(out, ob, w, 16ull * C) ||
-        overlap(out, ob, bias, 4ull * C) || overlap(out, ob, lens, 4ull * c.batch) ||
-        overlap(out, ob, s->base, s->lay.total_bytes))
+    const uint64_t ob = span(rows, C, C, 2), xb = span(rows, x_stride, C, 2);
+    if (in_state(s, x, xb) || in_state(s, w, 16ull * C) || in_state(s, bias, 4ull * C) || in_state(s, lens, 4ull * c.batch))
+        return api_fail(RMA_ERR_INVALID_ARG, "an input overlaps the state");
+    if (overlap(out, ob, x, xb) || overlap(out, ob, w, 16ull * C) ||
+        overlap(out, ob, bias, 4ull * C) || overlap(out, ob, lens, 4ull * c.batch) || in_state(s, out, ob))
         return api_fail(RMA_ERR_INVALID_ARG, "out overlaps an input or the state");
     rc = check_device(s->device);
     if (rc != RMA_OK) return rc;
@@ -336,7 +345,7 @@ int rma_gdn_prefill(rma_gdn_state* st, int layer, int n_tok, const uint16_t* qkv
     if (overlap(ws, need, qkv, span(rows, d.C, d.C, 2)) || overlap(ws, need, a, ab) || overlap(ws, need, b, ab) ||
         overlap(ws, need, a_log, 4ull * d.HV) || overlap(ws, need, dt_bias, 4ull * d.HV) ||
         overlap(ws, need, lens, 4ull * d.B) || overlap(ws, need, out, span(rows, d.HV * kGdnDim, d.HV * kGdnDim, 2)) ||
-        overlap(ws, need, s->base, s->lay.total_bytes))
+        in_state(s, ws, need))
         return api_fail(RMA_ERR_INVALID_ARG, "ws overlaps a tensor of the call or the state");
     rc = check_device(s->device);
     if (rc != RMA_OK) return rc;

@@ -385,6 +385,7 @@ typedef struct rma_gdn_config {
  *   conv    bf16 [n_layers][batch][3][C]      the last three raw input rows, oldest first
  *   delta   f32  [n_layers][batch][n_v_heads][128 (key)][128 (value)]
  *   status  u32  one word (RMA_STATUS_* bits)
+ * No tensor of a rma_gdn_* call may overlap the buffer (RMA_ERR_INVALID_ARG).
  * A sequence starts from zeros.  A caller may read and write both arrays
  * directly (a new sequence in a batch slot, a checkpoint) while no call is in
  * flight. */

@@ -316,7 +316,7 @@ def test_long_blocks_of_few_heads(batch, hk, hv, n, lens):
 
 
 @pytest.mark.parametrize("batch,hk,hv,n,lens", [(1, 1, 2, 2049, None), (3, 2, 4, 2100, [2100, 0, 1990]), (2, 3, 9, 2050, [777, 2050]),
-                                                (1, 5, 5, 1985, None)])
+                                                (1, 5, 5, 1985, None), (1, 1, 9, 2000, [1999])])
 def test_blocks_long_enough_for_one_launch(batch, hk, hv, n, lens):
     """32 chunks and more of few heads go in one launch: against the oracle, whatever the workspace held (its flags
     among it), with NaN in the padding, and the same bits every time."""
@@ -574,6 +574,30 @@ def test_gdn_refusals():
         st.workspace(0)
     with pytest.raises(rma.RmaError):
         st.workspace(1 << 24)
+    torch.cuda.synchronize()
+    assert torch.equal(before, st.buffer)
+
+
+def test_gdn_inputs_inside_the_state_are_refused():
+    """A call updates its state while it reads its inputs, so none may lie there."""
+    rma, st, d, x = delta_case(2, 1, 1, 2, seed=93)
+    out, y = torch.empty(2, 2, 128, dtype=BF, device="cuda"), torch.empty(2, 512, dtype=BF, device="cuda")
+    w = torch.zeros(512, 4, device="cuda")
+    flat = st.delta.view(-1)
+    gates = flat[:2].view(BF).view(2, 2)
+    good = dict(qkv=d["qkv"], a=d["a"], b=d["b"], a_log=d["a_log"], dt_bias=d["dt_bias"], out=out)
+    before = st.buffer.clone()
+    for change in (dict(qkv=st.conv.view(-1)[:1024].view(2, 512)),
+                   dict(a=gates), dict(b=gates), dict(a_log=flat[:2]), dict(dt_bias=flat[2:4]), dict(out=flat[:256].view(BF).view(2, 2, 128))):
+        for call, more in (("gdn_decode_step", {}), ("gdn_prefill", dict(ws=st.workspace(1)))):
+            with pytest.raises(rma.RmaError) as e:
+                getattr(rma, call)(st, 0, **(good | change | more))
+            assert e.value.code == -1
+    for change in (dict(x=st.conv.view(-1)[:1024].view(2, 512)), dict(w=flat[:2048].view(512, 4)), dict(bias=flat[:512]),
+                   dict(lens=flat[:2].view(torch.int32))):
+        with pytest.raises(rma.RmaError) as e:
+            rma.gdn_conv(st, 0, **(dict(x=d["qkv"], w=w, out=y) | change))
+        assert e.value.code == -1
     torch.cuda.synchronize()
     assert torch.equal(before, st.buffer)
 
