@@ -23,9 +23,10 @@
 // Precision.  The state is carried on, so its products keep FP32's precision: the factors that change
 // (S0, X, U) and T go to the tensor cores as pairs of FP16 (hi + lo, 22 bits), each lane or row scaled by
 // a power of two so that its largest value is near FP16's upper end, which leaves 2^-39 of the largest as
-// the smallest step.  K and Q are BF16 values, which are exact in FP16 once their row is scaled the same
-// way, and the norms are factors of the rows.  Products of two pairs leave out lo x lo (2^-22).  What
-// only reaches the BF16 output (Q S0 and P U) takes hi alone, 2^-11, an eighth of the output's own rounding.
+// the smallest step.  K and Q are BF16 values, which FP16 holds exactly, once their row is scaled the same way, down to
+// 2^-20 of the row's largest, and to 2^-28 of it below; the norms are factors of the rows.  Products of two pairs leave
+// out lo x lo (2^-22).  The products that only reach the output (Q S0 and P U) are made of pairs as well: with the high
+// parts alone, 2^-12 of each term, one output in nine was rounded to a neighbour of what FP32 gives (now 1 in 5,000).
 // Decays are e^(difference of sums): the sums are FP64, since a strong decay (g down to -128) next to a
 // weak one would take the weak one's digits in FP32.
 #include <cuda.h>
@@ -41,7 +42,8 @@ constexpr int kC = 64;                        // tokens of a chunk
 constexpr int kTile = kC * 128;               // 64 rows of 64 FP16: one operand image
 // a (chunk, key head) block of the workspace: K columns 0-63, 64-127, Q columns 0-63, 64-127
 constexpr int kKQBytes = 4 * kTile;
-// a (chunk, value head) block: T hi, T lo, P, then FP32 scalars
+// a (chunk, value head) block: T hi, T lo, P hi, then FP32 scalars.  All are lower triangular, so rows 0-31 of
+// columns 32-63 are zeros that no product takes: P lo's three quarters stand there (p_lo_at).
 constexpr int kTPBytes = 3 * kTile + 1024;
 constexpr int kOffTLo = kTile, kOffP = 2 * kTile, kOffScal = 3 * kTile;
 // scalars: factors of token i in W (c1), Q S0 (c2) and U' (c3); then single values: e^{G_C}, the inverse
@@ -111,6 +113,10 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 
 // byte offset of 16-byte piece `piece` (8 values) of row `row` in an operand image
 __device__ __forceinline__ int piece_at(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+// where a piece of P lo stands in a (chunk, value head) block; rows 0-31 have pieces 0-3 only
+__device__ __forceinline__ int p_lo_at(int row, int piece) {
+    return (row < 32 ? kOffP : (piece < 4 ? 0 : kOffTLo)) + piece_at(row & 31, piece | 4);
+}
 
 // ---------------------------------------------------------------------------
 // launch 1
@@ -535,8 +541,13 @@ __device__ __forceinline__ void prep_item(const DeltaArgs& a, PrepSmem& s, int N
                     }
                     *reinterpret_cast<float4*>(&T[i][8 * p]) = make_float4(A[0], A[1], A[2], A[3]);
                     *reinterpret_cast<float4*>(&T[i][8 * p + 4]) = make_float4(A[4], A[5], A[6], A[7]);
-                    *reinterpret_cast<uint4*>(out + kOffP + piece_at(i, p)) =
-                        make_uint4(half2_bits(P[0], P[1]), half2_bits(P[2], P[3]), half2_bits(P[4], P[5]), half2_bits(P[6], P[7]));
+                    if (i >= 32 || p < 4) {
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) split2(P[2 * x], P[2 * x + 1], hi[x], lo[x]);
+                        *reinterpret_cast<uint4*>(out + kOffP + piece_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(out + p_lo_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
             }
             {
@@ -554,8 +565,11 @@ __device__ __forceinline__ void prep_item(const DeltaArgs& a, PrepSmem& s, int N
                     P[x] = j <= i ? fp * d * qk[x] : 0.f;
                 }
                 *reinterpret_cast<float4*>(&T[i][j0]) = make_float4(A[0], A[1], A[2], A[3]);
-                *reinterpret_cast<uint2*>(out + kOffP + piece_at(i, i >> 3) + 8 * (gt & 1)) =
-                    make_uint2(half2_bits(P[0], P[1]), half2_bits(P[2], P[3]));
+                uint32_t hi[2], lo[2];
+                split2(P[0], P[1], hi[0], lo[0]);
+                split2(P[2], P[3], hi[1], lo[1]);
+                *reinterpret_cast<uint2*>(out + kOffP + piece_at(i, i >> 3) + 8 * (gt & 1)) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(out + p_lo_at(i, i >> 3) + 8 * (gt & 1)) = make_uint2(lo[0], lo[1]);
             }
             if (gt < kC) {
                 const float since = ex2(Gh[gt] + Gl[gt]);
@@ -602,8 +616,10 @@ __device__ __forceinline__ void prep_item(const DeltaArgs& a, PrepSmem& s, int N
                         sum += fabsf(v[2 * x]) + fabsf(v[2 * x + 1]);
                         split2(v[2 * x] * sc, v[2 * x + 1] * sc, hi[x], lo[x]);
                     }
-                    *reinterpret_cast<uint4*>(out + piece_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4*>(out + kOffTLo + piece_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    if (i >= 32 || p < 4) {   // elsewhere P lo stands
+                        *reinterpret_cast<uint4*>(out + piece_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(out + kOffTLo + piece_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
                     if (p == 0) s.tsum[grp][i] = sum;
@@ -681,7 +697,7 @@ static_assert(kScanSmem <= 227 * 1024, "shared memory per CTA");
 //   S   [0, 128)    per half: S0 as hi, lo (32 + 32); then the state's increment (64, FP32)
 //   W   [128, 192)  per half: W (32); then the scaled U as hi, lo (16 + 16)
 //   X   [192, 256)  per half: X as hi, lo (16 + 16)
-//   U   [256, 320)  per half: U (32); then U as hi (16)
+//   U   [256, 320)  per half: U (32); then U as hi, lo (16 + 16)
 //   Q S0 [320, 384),  P U [384, 448)
 constexpr uint32_t kTmS = 0, kTmW = 128, kTmX = 192, kTmU = 256, kTmQ = 320, kTmP = 384, kTmCols = 512;
 
@@ -917,8 +933,8 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 }
                 if (c > 0 && !wait(kbO, c - 1)) break;
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    ptx::mma_ts1(kTmQ, kTmS + 64 * (ks >> 2) + 8 * (ks & 3), dk + (2 + (ks >> 2)) * kImage + 2 * (ks & 3), id64, ks > 0, go);
+                for (int ks = 0; ks < 16; ++ks)   // per half of the keys: hi, then lo
+                    ptx::mma_ts1(kTmQ, kTmS + 8 * ks, dk + (2 + (ks >> 3)) * kImage + 2 * (ks & 3), id64, ks > 0, go);
                 // U: the first half's X for all tokens, which is all of the first half's U; then the second half's
                 if (!wait(kbX, c)) break;
 #pragma unroll
@@ -944,9 +960,17 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                     ptx::mma_ts1(kTmS, kTmW + 8 * ks, dd + 128 * ks, id128t, ks > 0, go);
                     ptx::mma_ts1(kTmS, kTmW + 16 + 8 * ks, dd + 128 * ks, id128t, 1, go);
                 }
+                // P U by quarters, as P lo stands: the first half's U for each half of the tokens, then the second's
+                auto pu = [&](int ht, int hu, uint32_t p_hi, uint32_t p_lo, bool first) {
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-                    ptx::mma_ts1(kTmP, kTmU + 8 * ks, dt + kP + 2 * ks, id64, ks > 0, go);
+                    for (int ks = 0; ks < 2; ++ks) {
+                        ptx::mma_ts1(kTmP + 32 * ht, kTmU + 32 * hu + 8 * ks, p_hi + 2 * ks, id32, !first || ks > 0, go);
+                        ptx::mma_ts1(kTmP + 32 * ht, kTmU + 32 * hu + 16 + 8 * ks, p_hi + 2 * ks, id32, 1, go);
+                        ptx::mma_ts1(kTmP + 32 * ht, kTmU + 32 * hu + 8 * ks, p_lo + 2 * ks, id32, 1, go);
+                    }
+                };
+                pu(0, 0, dt + kP, dt + kP + 4, true);
+                pu(1, 0, dt + kP + kHalfRows, dt + 4, true);
                 if (!wait(kbU + 1, c)) break;
 #pragma unroll
                 for (int hk = 0; hk < 2; ++hk) {
@@ -958,9 +982,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                     }
                     ptx::mma_commit1(&bars[kbDDone + hk], go);
                 }
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-                    ptx::mma_ts1(kTmP + 32, kTmU + 32 + 8 * ks, dt + kP + kHalfRows + 4 + 2 * ks, id32, 1, go);
+                pu(1, 1, dt + kP + kHalfRows + 4, dt + kTLo + 4, false);
                 ptx::mma_commit1(&bars[kbPDone], go);
             }
             ptx::mma_commit1(&bars[kbDrain], go);
@@ -1160,22 +1182,21 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             ptx::tmem_wait_ld();
             {
                 const f2 cu2 = pack2(cu, cu), cd2 = pack2(cd, cd);
-                uint32_t hi[16], lo[16], u[16];
+                uint32_t hi[16], lo[16];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
                     f2 c3[2];
                     lds4(scal + kC3 + 2 * i, c3[0], c3[1]);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const f2 y = pack2(x[2 * (i + j)], x[2 * (i + j) + 1]);
-                        const float2 z = unpack2(mul2(y, cu2));
-                        u[i + j] = half2_bits(z.x, z.y);
-                        split2(mul2(y, mul2(c3[j], cd2)), hi[i + j], lo[i + j]);
-                    }
+                    for (int j = 0; j < 2; ++j)
+                        split2(mul2(pack2(x[2 * (i + j)], x[2 * (i + j) + 1]), mul2(c3[j], cd2)), hi[i + j], lo[i + j]);
                 }
                 ptx::tmem_st16(tl + kTmW + 32 * wg, hi);
                 ptx::tmem_st16(tl + kTmW + 32 * wg + 16, lo);
-                ptx::tmem_st16(tl + kTmU + 32 * wg, u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) split2(mul2(pack2(x[2 * i], x[2 * i + 1]), cu2), hi[i], lo[i]);
+                ptx::tmem_st16(tl + kTmU + 32 * wg, hi);
+                ptx::tmem_st16(tl + kTmU + 32 * wg + 16, lo);
                 signal(kbU);
             }
             if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);   // (the output warps wait for the products)
