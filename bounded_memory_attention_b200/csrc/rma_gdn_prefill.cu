@@ -42,10 +42,11 @@ constexpr int kC = 64;                        // tokens of a chunk
 constexpr int kTile = kC * 128;               // 64 rows of 64 FP16: one operand image
 // a (chunk, key head) block of the workspace: K columns 0-63, 64-127, Q columns 0-63, 64-127
 constexpr int kKQBytes = 4 * kTile;
-// a (chunk, value head) block: T hi, T lo, P hi, then FP32 scalars.  All are lower triangular, so rows 0-31 of
-// columns 32-63 are zeros that no product takes: P lo's three quarters stand there (p_lo_at).
+// a (chunk, value head) block: T (hi and lo by turns, 8 rows each), P hi, then FP32 scalars.  All are lower triangular,
+// so rows 0-31 of columns 32-63 are zeros that no product takes.  P lo stands there: its columns 0-31 in the places
+// of T's, 8 rows after 8 rows, the rest in those of P hi.
 constexpr int kTPBytes = 3 * kTile + 1024;
-constexpr int kOffTLo = kTile, kOffP = 2 * kTile, kOffScal = 3 * kTile;
+constexpr int kOffTLo = 1024, kOffP = 2 * kTile, kOffScal = 3 * kTile;
 // scalars: factors of token i in W (c1), Q S0 (c2) and U' (c3); then single values: e^{G_C}, the inverse
 // scales of T and P, and the bounds that the scan takes its scales from (see there)
 constexpr int kC1 = 0, kC2 = 64, kC3 = 128, kEC = 192, kTS = 193, kPS = 194, kBW = 196, kBT = 197, kBS = 198;
@@ -113,9 +114,11 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
 
 // byte offset of 16-byte piece `piece` (8 values) of row `row` in an operand image
 __device__ __forceinline__ int piece_at(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+// the same of T hi
+__device__ __forceinline__ int t_at(int row, int piece) { return piece_at(row, piece) + (row >> 3) * 1024; }
 // where a piece of P lo stands in a (chunk, value head) block; rows 0-31 have pieces 0-3 only
 __device__ __forceinline__ int p_lo_at(int row, int piece) {
-    return (row < 32 ? kOffP : (piece < 4 ? 0 : kOffTLo)) + piece_at(row & 31, piece | 4);
+    return piece < 4 ? piece_at(row, piece + 4) : kOffP + piece_at(row - 32, piece);
 }
 
 // ---------------------------------------------------------------------------
@@ -617,8 +620,8 @@ __device__ __forceinline__ void prep_item(const DeltaArgs& a, PrepSmem& s, int N
                         split2(v[2 * x] * sc, v[2 * x + 1] * sc, hi[x], lo[x]);
                     }
                     if (i >= 32 || p < 4) {   // elsewhere P lo stands
-                        *reinterpret_cast<uint4*>(out + piece_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(out + kOffTLo + piece_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        *reinterpret_cast<uint4*>(out + t_at(i, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(out + kOffTLo + t_at(i, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
 #pragma unroll
                     for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -697,9 +700,33 @@ static_assert(kScanSmem <= 227 * 1024, "shared memory per CTA");
 //   S   [0, 128)    per half: S0 as hi, lo (32 + 32); then the state's increment (64, FP32)
 //   W   [128, 192)  per half: W (32); then the scaled U as hi, lo (16 + 16)
 //   X   [192, 256)  per half: X as hi, lo (16 + 16)
-//   U   [256, 320)  per half: U (32); then U as hi, lo (16 + 16)
-//   Q S0 [320, 384),  P U [384, 448)
-constexpr uint32_t kTmS = 0, kTmW = 128, kTmX = 192, kTmU = 256, kTmQ = 320, kTmP = 384, kTmCols = 512;
+//   U   [256, 320)  U by the first half's X; then per half U as hi, lo (16 + 16)
+//   Q S0 [320, 384),  P U [384, 448) by the first half's U
+//   [448, 480) U of the second half's tokens by their own X,  [480, 512) their P U by their own U
+constexpr uint32_t kTmS = 0, kTmW = 128, kTmX = 192, kTmU = 256, kTmCols = 512;
+
+// The accumulators: first column and width.  Products onto one accumulator follow one another without a commit and a
+// wait between them, which the architecture promises to keep in order only where accumulator and shape are the same.  So
+// each has one width, none shares a column with another, and products take them from here alone.
+struct Accumulator {
+    uint32_t column, width;
+};
+enum { kAccD, kAccW, kAccU, kAccQ, kAccP, kAccU2, kAccP2, kAccumulators };
+constexpr Accumulator kAcc[kAccumulators] = {{kTmS, 128}, {kTmW, 64}, {kTmU, 64}, {320, 64}, {384, 64}, {448, 32}, {480, 32}};
+constexpr bool disjoint() {
+    for (int i = 0; i < kAccumulators; ++i) {
+        if (kAcc[i].column + kAcc[i].width > kTmCols) return false;
+        for (int j = 0; j < i; ++j)
+            if (kAcc[i].column < kAcc[j].column + kAcc[j].width && kAcc[j].column < kAcc[i].column + kAcc[i].width) return false;
+    }
+    return true;
+}
+static_assert(disjoint(), "two accumulators share columns");
+// D[tmem] (+)= A[tmem] * B, M = 128, B's rows (or columns, if transposed) in eights kStride bytes apart
+template <int kA, bool kTransposed = false, uint32_t kStride = 1024>
+__device__ __forceinline__ void product(uint32_t a_tmem, uint32_t b, bool add, uint32_t go) {
+    ptx::mma_ts1<kStride>(kAcc[kA].column, a_tmem, b, ptx::idesc_f16_f32(128, kAcc[kA].width, false, kTransposed), add, go);
+}
 
 // named barriers: a half's lane maxima offered by a warp to the other half's (8), the output warps,
 // a warp and the other half's (4)
@@ -712,12 +739,12 @@ enum ScanBar {
     kbX = 8,         // [2] 4 warps: X
     kbU = 10,        // [2] 4 warps: U and the scaled U
     kbO = 12,        // 4 warps: Q S0 and P U read
-    kbWDone = 13,    // [2] commits: W of a half's tokens
-    kbUDone = 15,    // [2] U of a half's tokens (and all before, Q S0 among it)
-    kbDDone = 17,    // [2] the state's increment, a half of the keys
-    kbPDone = 19,    // P U, and with it every product of the chunk
-    kbDrain = 20,    // commit after the last product, also of an abandoned CTA
-    kScanBars = 21
+    kbWDone = 13,    // commits: W
+    kbUDone = 14,    // [2] U of a half's tokens (and all before, Q S0 among it)
+    kbDDone = 16,    // the state's increment
+    kbPDone = 17,    // P U, and with it every product of the chunk
+    kbDrain = 18,    // commit after the last product, also of an abandoned CTA
+    kScanBars = 19
 };
 
 struct ScanMaps {
@@ -750,6 +777,11 @@ __device__ __forceinline__ float2 unpack2(f2 v) {
 __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     f2 r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
@@ -895,12 +927,10 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             // ---------------- products ----------------
             // The warp computes the operands together and one elected lane issues: a branch taken by one
             // lane instead costs about 100 cycles an instruction, three times what its product takes.
-            // T and P are lower triangular: the first half's tokens take the first half's rows and columns only.
-            constexpr uint32_t id32 = ptx::idesc_f16_f32(128, 32, false, false);
-            constexpr uint32_t id64 = ptx::idesc_f16_f32(128, 64, false, false);
-            constexpr uint32_t id64t = ptx::idesc_f16_f32(128, 64, false, true);
-            constexpr uint32_t id128t = ptx::idesc_f16_f32(128, 128, false, true);
-            constexpr uint32_t kImage = kTile >> 4, kHalfRows = (32 * 128) >> 4, kTLo = kOffTLo >> 4, kP = kOffP >> 4;
+            // T and P are lower triangular: the first half's tokens take the first half's rows and columns only, and
+            // what the second half's add for their own goes to accumulators of its own.  An instruction takes about 39
+            // cycles with 64 or 32 columns, 64 with 128.
+            constexpr uint32_t kImage = kTile >> 4, kHalfRows = (32 * 128) >> 4, kHalfT = 2 * kHalfRows, kTStride = 2048, kTLo = kOffTLo >> 4, kP = kOffP >> 4;
             const uint32_t go = ptx::elect_one();
             // (The loop over the chunks is not unrolled by stage: three copies of it crowd the other roles out of
             // the instruction caches, which costs more than constant operands save.)
@@ -918,71 +948,67 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 if (!wait(kbFull + st, c / kStages)) break;
                 // the chunk before is complete: the scaled U lies where W goes
                 if (c > 0 && !wait(kbPDone, c - 1)) break;
-                // W, as the halves of the state arrive; the first half's tokens are done first
+                // W, as the halves of the state arrive
                 if (!wait(kbS, c)) break;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)   // hi, then lo
-                    ptx::mma_ts1(kTmW, kTmS + 8 * ks, dk + 2 * (ks & 3), id64, ks > 0, go);
+                    product<kAccW>(kTmS + 8 * ks, dk + 2 * (ks & 3), ks > 0, go);
                 if (!wait(kbS + 1, c)) break;
 #pragma unroll
-                for (int ht = 0; ht < 2; ++ht) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        ptx::mma_ts1(kTmW + 32 * ht, kTmS + 64 + 8 * ks, dk + kImage + ht * kHalfRows + 2 * (ks & 3), id32, 1, go);
-                    ptx::mma_commit1(&bars[kbWDone + ht], go);
-                }
+                for (int ks = 0; ks < 8; ++ks)
+                    product<kAccW>(kTmS + 64 + 8 * ks, dk + kImage + 2 * (ks & 3), true, go);
+                ptx::mma_commit1(&bars[kbWDone], go);
                 if (c > 0 && !wait(kbO, c - 1)) break;
 #pragma unroll
                 for (int ks = 0; ks < 16; ++ks)   // per half of the keys: hi, then lo
-                    ptx::mma_ts1(kTmQ, kTmS + 8 * ks, dk + (2 + (ks >> 3)) * kImage + 2 * (ks & 3), id64, ks > 0, go);
-                // U: the first half's X for all tokens, which is all of the first half's U; then the second half's
+                    product<kAccQ>(kTmS + 8 * ks, dk + (2 + (ks >> 3)) * kImage + 2 * (ks & 3), ks > 0, go);
+                // U: the first half's X for all tokens, then the second half's for its own
                 if (!wait(kbX, c)) break;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    ptx::mma_ts1(kTmU, kTmX + 8 * ks, dt + 2 * ks, id64, ks > 0, go);
-                    ptx::mma_ts1(kTmU, kTmX + 16 + 8 * ks, dt + 2 * ks, id64, 1, go);
-                    ptx::mma_ts1(kTmU, kTmX + 8 * ks, dt + kTLo + 2 * ks, id64, 1, go);
+                    const uint32_t x = kTmX + 8 * ks, t = dt + 2 * ks;
+                    product<kAccU, false, kTStride>(x, t, ks > 0, go);
+                    product<kAccU, false, kTStride>(x + 16, t, true, go);
+                    product<kAccU, false, kTStride>(x, t + kTLo, true, go);
                 }
                 ptx::mma_commit1(&bars[kbUDone], go);
                 if (!wait(kbX + 1, c)) break;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    const uint32_t t = dt + kHalfRows + 4 + 2 * ks;
-                    ptx::mma_ts1(kTmU + 32, kTmX + 32 + 8 * ks, t, id32, 1, go);
-                    ptx::mma_ts1(kTmU + 32, kTmX + 48 + 8 * ks, t, id32, 1, go);
-                    ptx::mma_ts1(kTmU + 32, kTmX + 32 + 8 * ks, t + kTLo, id32, 1, go);
+                    const uint32_t x = kTmX + 32 + 8 * ks, t = dt + kHalfT + 4 + 2 * ks;
+                    product<kAccU2, false, kTStride>(x, t, ks > 0, go);
+                    product<kAccU2, false, kTStride>(x + 16, t, true, go);
+                    product<kAccU2, false, kTStride>(x, t + kTLo, true, go);
                 }
                 ptx::mma_commit1(&bars[kbUDone + 1], go);
-                // the state's increment: the first half's tokens for all keys, then the second's for each half of them
-                if (!wait(kbU, c)) break;
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {   // 16 rows are 2 KiB
-                    ptx::mma_ts1(kTmS, kTmW + 8 * ks, dd + 128 * ks, id128t, ks > 0, go);
-                    ptx::mma_ts1(kTmS, kTmW + 16 + 8 * ks, dd + 128 * ks, id128t, 1, go);
-                }
-                // P U by quarters, as P lo stands: the first half's U for each half of the tokens, then the second's
-                auto pu = [&](int ht, int hu, uint32_t p_hi, uint32_t p_lo, bool first) {
+                // the state's increment, a half of the tokens after the other (16 rows of K are 2 KiB)
+                auto increment = [&](int h) {
 #pragma unroll
                     for (int ks = 0; ks < 2; ++ks) {
-                        ptx::mma_ts1(kTmP + 32 * ht, kTmU + 32 * hu + 8 * ks, p_hi + 2 * ks, id32, !first || ks > 0, go);
-                        ptx::mma_ts1(kTmP + 32 * ht, kTmU + 32 * hu + 16 + 8 * ks, p_hi + 2 * ks, id32, 1, go);
-                        ptx::mma_ts1(kTmP + 32 * ht, kTmU + 32 * hu + 8 * ks, p_lo + 2 * ks, id32, 1, go);
+                        product<kAccD, true>(kTmW + 32 * h + 8 * ks, dd + 128 * (2 * h + ks), h > 0 || ks > 0, go);
+                        product<kAccD, true>(kTmW + 32 * h + 16 + 8 * ks, dd + 128 * (2 * h + ks), true, go);
                     }
                 };
-                pu(0, 0, dt + kP, dt + kP + 4, true);
-                pu(1, 0, dt + kP + kHalfRows, dt + 4, true);
+                if (!wait(kbU, c)) break;
+                increment(0);
                 if (!wait(kbU + 1, c)) break;
+                increment(1);
+                ptx::mma_commit1(&bars[kbDDone], go);
+                // P U, as U
 #pragma unroll
-                for (int hk = 0; hk < 2; ++hk) {
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks) {
-                        const uint32_t k = dd + hk * kImage + 128 * (2 + ks);
-                        ptx::mma_ts1(kTmS + 64 * hk, kTmW + 32 + 8 * ks, k, id64t, 1, go);
-                        ptx::mma_ts1(kTmS + 64 * hk, kTmW + 48 + 8 * ks, k, id64t, 1, go);
-                    }
-                    ptx::mma_commit1(&bars[kbDDone + hk], go);
+                for (int ks = 0; ks < 2; ++ks) {
+                    const uint32_t u = kTmU + 8 * ks, p = dt + kP + 2 * ks;
+                    product<kAccP>(u, p, ks > 0, go);
+                    product<kAccP>(u + 16, p, true, go);
+                    product<kAccP>(u, dt + 4 + 2 * ks, true, go);
                 }
-                pu(1, 1, dt + kP + kHalfRows + 4, dt + kTLo + 4, false);
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const uint32_t u = kTmU + 32 + 8 * ks, p = dt + kP + kHalfRows + 4 + 2 * ks;
+                    product<kAccP2>(u, p, ks > 0, go);
+                    product<kAccP2>(u + 16, p, true, go);
+                    product<kAccP2>(u, dt + kP + 4 + 2 * ks, true, go);
+                }
                 ptx::mma_commit1(&bars[kbPDone], go);
             }
             ptx::mma_commit1(&bars[kbDrain], go);
@@ -1020,8 +1046,15 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {           // 32 tokens
                     uint32_t q[16], y[16], o[8];
-                    ptx::tmem_ld_frag4(tl + ((uint32_t)(16 * hl) << 16) + kTmQ + 32 * p, q);
-                    ptx::tmem_ld_frag4(tl + ((uint32_t)(16 * hl) << 16) + kTmP + 32 * p, y);
+                    ptx::tmem_ld_frag4(tl + ((uint32_t)(16 * hl) << 16) + kAcc[kAccQ].column + 32 * p, q);
+                    ptx::tmem_ld_frag4(tl + ((uint32_t)(16 * hl) << 16) + kAcc[kAccP].column + 32 * p, y);
+                    if (p == 1) {                       // by both halves' U
+                        uint32_t z[16];
+                        ptx::tmem_ld_frag4(tl + ((uint32_t)(16 * hl) << 16) + kAcc[kAccP2].column, z);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) + __uint_as_float(z[i]));
+                    }
                     ptx::tmem_wait_ld();
                     if (hl == 1 && p == 1) {            // Q S0 and P U are read
                         ptx::tc_fence_before();
@@ -1156,7 +1189,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             }
             // X
             // (an abandoned CTA goes on through its barriers, on values that nobody uses)
-            ok = ptx::mbar_wait_warp(&bars[kbWDone + wg], c & 1, abort_flag, a.status) && ok;
+            ok = ptx::mbar_wait_warp(&bars[kbWDone], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmW + 32 * wg, x);
             ptx::tmem_wait_ld();
@@ -1179,7 +1212,19 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             ok = ptx::mbar_wait_warp(&bars[kbUDone + wg], c & 1, abort_flag, a.status) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmU + 32 * wg, x);
-            ptx::tmem_wait_ld();
+            if (wg == 1) {   // by both halves' X
+                uint32_t y[32];
+                ptx::tmem_ld32(tl + kAcc[kAccU2].column, y);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 z = unpack2(add2(pack2(x[2 * i], x[2 * i + 1]), pack2(y[2 * i], y[2 * i + 1])));
+                    x[2 * i] = __float_as_uint(z.x);
+                    x[2 * i + 1] = __float_as_uint(z.y);
+                }
+            } else {
+                ptx::tmem_wait_ld();
+            }
             {
                 const f2 cu2 = pack2(cu, cu), cd2 = pack2(cd, cd);
                 uint32_t hi[16], lo[16];
@@ -1208,7 +1253,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             }
             // the state
             if (c >= 0) {
-                ok = ptx::mbar_wait_warp(&bars[kbDDone + wg], c & 1, abort_flag, a.status) && ok;
+                ok = ptx::mbar_wait_warp(&bars[kbDDone], c & 1, abort_flag, a.status) && ok;
                 ptx::tc_fence_after();
                 es = es1;
                 const f2 k2 = pack2(ck, ck);

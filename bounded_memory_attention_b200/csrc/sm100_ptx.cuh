@@ -208,11 +208,12 @@ __device__ __forceinline__ uint32_t elect_one() {
     return r;
 }
 // D[tmem] (+)= A[tmem] * B; M = 128.  Executed by a whole warp, issued by the lane with go != 0.  B's
-// descriptor has the 128-byte swizzle, version 1 and a stride of 1,024 bytes in its high word; b_lo is its low
-// word, address >> 4 | leading offset >> 4 << 16.
+// descriptor has the 128-byte swizzle, version 1 and a stride of kStride bytes (from 8 rows to the next 8) in its
+// high word; b_lo is its low word, address >> 4 | leading offset >> 4 << 16.
+template <uint32_t kStride = 1024>
 __device__ __forceinline__ void mma_ts1(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
                                         uint32_t accumulate, uint32_t go) {
-    constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+    constexpr uint32_t kHigh = (kStride >> 4) | (1u << 14) | (2u << 29);
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
         "mov.b64 b, {%2, %6};\n\t"
