@@ -728,14 +728,14 @@ __device__ __forceinline__ void product(uint32_t a_tmem, uint32_t b, bool add, u
     ptx::mma_ts1<kStride>(kAcc[kA].column, a_tmem, b, ptx::idesc_f16_f32(128, kAcc[kA].width, false, kTransposed), add, go);
 }
 
-// named barriers: a half's lane maxima offered by a warp to the other half's (8), the output warps,
-// a warp and the other half's (4)
-constexpr int kBarPair = 1, kBarOut = 9, kBarBoth = 10;
+// named barriers: the output warps, once a chunk; a warp and the other half's, twice in all (4).  No thread passes one more
+// or fewer times after it has given up on a wait than before.
+constexpr int kBarOut = 1, kBarBoth = 2;
 
 enum ScanBar {
     kbFull = 0,      // [3] the stage's loads landed (tx bytes)
     kbEmpty = 3,     // [3] 8 warps and the stores are done with the stage (and every product that reads it)
-    kbS = 6,         // [2] 4 warps: their half of S0 in tensor memory
+    kbS = 6,         // [2] 4 warps: their half of S0 in tensor memory, and their lane maxima
     kbX = 8,         // [2] 4 warps: X
     kbU = 10,        // [2] 4 warps: U and the scaled U
     kbO = 12,        // 4 warps: Q S0 and P U read
@@ -751,6 +751,8 @@ struct ScanMaps {
     CUtensorMap v;     // qkv as [batch n][C]: boxes of 128 columns x 64 rows, linear
     CUtensorMap out;   // out as [batch n][HV 128]: boxes of 64 columns x 64 rows, 128-byte swizzle
 };
+
+static_assert(8 * kScanBars + 8 <= kScanMax - kScanBar, "barriers, tensor memory's address and the abort flag");
 
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
@@ -1107,14 +1109,15 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars[bar + wg]);
         };
-        // this half's largest values of the lane's state and V, offered to the other half and taken from it
+        // this half's largest values of the lane's state and V, offered to the other half and taken from it.  What the
+        // other half has offered for a chunk is there when its state is (kbS): a bounded wait, as all that stand
+        // between the chunks.  (By named barriers, two arrivals of a warp that has given up on its waits could complete
+        // one without the other half's warp, which would then wait for good.)
         auto offer = [&](float ms, float mv) {
             maxima[wg * 128 + row] = ms;
             maxima[(2 + wg) * 128 + row] = mv;
-            ptx::named_bar_arrive(kBarPair + 4 * wg + w, 64);
         };
         auto take = [&](float& ms, float& mv) {
-            ptx::named_bar_sync(kBarPair + 4 * (wg ^ 1) + w, 64);
             ms = fmaxf(ms, maxima[(wg ^ 1) * 128 + row]);
             mv = fmaxf(mv, maxima[(2 + (wg ^ 1)) * 128 + row]);
         };
@@ -1150,6 +1153,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
 #pragma unroll
             for (int i = 0; i < 32; ++i) smax = absmax(smax, S[i]);
             offer(smax, 0.f);
+            ptx::named_bar_sync(kBarBoth + w, 64);
             take(smax, vmax);
             ptx::named_bar_sync(kBarBoth + w, 64);   // both have taken, before the next offer
             es = scale_exponent(smax, 15);
@@ -1170,6 +1174,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             const float* one = reinterpret_cast<const float*>(smem + st * kStageBytes + kStageTP + kOffScal);
             const float* scal = one + 32 * wg;   // this half's tokens
             // while W is computed: the bounds and the scales
+            ok = ptx::mbar_wait_warp(&bars[kbS + (wg ^ 1)], c & 1, abort_flag, a.status) && ok;
             take(smax, vmax);
             const float inv_s = pow2(-es);
             smax *= inv_s;
