@@ -1081,7 +1081,10 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             }
             ptx::fence_proxy_async_smem();
             ptx::named_bar_sync(kBarOut, 128);
-            if (left >= kC) {
+            ok = ok && *abort_flag == 0;   // a wait that gave up in another of these warps, too
+            if (!ok) {
+                // an abandoned CTA: what stands in the stage is nobody's output
+            } else if (left >= kC) {
                 if (warp == kWarpOut && lane < 2) {
                     tma_store_2d(&maps.out, stage + kStageV + lane * kTile, h * kGdnDim + 64 * lane, b * a.n + c * kC);
                     ptx::bulk_commit();

@@ -39,3 +39,13 @@ def test_the_kernel_hands_over_with_the_state():
     src = open(SOURCE).read()
     assert "named_bar_arrive" not in src
     assert "mbar_wait_warp(&bars[kbS + (wg ^ 1)], c & 1, abort_flag" in src
+
+
+def test_an_abandoned_cta_stores_no_outputs():
+    """Every store of the output warps, and of the state, stands behind the verdict of the waits before it."""
+    src = open(SOURCE).read()
+    out = src[src.index("ptx::named_bar_sync(kBarOut, 128)"):src.index("ptx::mbar_arrive(&bars[kbEmpty + st])")]
+    guard = out.index("if (!ok)")
+    assert out.index("*abort_flag") < guard < out.index("} else if (left >= kC) {") < out.index("tma_store_2d")
+    last = src[src.rindex("if (ok) {"):]
+    assert last.index("gs[2 * i * kGdnDim] =") < last.index("__syncthreads")
