@@ -276,11 +276,40 @@ __global__ void __launch_bounds__(kRecThreads) gdn_recurrent_kernel(const __grid
             kk += __shfl_xor_sync(0xffffffffu, kk, o);
             kq += __shfl_xor_sync(0xffffffffu, kq, o);
         }
-        const float rq = (a.l2norm ? 1.f / sqrtf(qq + a.l2_eps) : 1.f) * a.scale;
-        const float rk = a.l2norm ? 1.f / sqrtf(kk + a.l2_eps) : 1.f;
-        kq *= rq * rk;
-        if (warp == 0) *reinterpret_cast<float4*>(&sk[buf][4 * lane]) = make_float4(ka.x * rk, ka.y * rk, kb.x * rk, kb.y * rk);
-        if (warp == 1) *reinterpret_cast<float4*>(&sq[buf][4 * lane]) = make_float4(qa.x * rq, qa.y * rq, qb.x * rq, qb.y * rq);
+        float4 kv = make_float4(ka.x, ka.y, kb.x, kb.y), qv = make_float4(qa.x, qa.y, qb.x, qb.y);
+        float rq, rk, fu = 1.f;   // fu: a factor of k.q that is applied to u first
+        if (a.l2norm ? plain_sum(qq + a.l2_eps) && plain_sum(kk + a.l2_eps) : qq < 0x1p110f && kk < 0x1p110f) {
+            rq = (a.l2norm ? 1.f / sqrtf(qq + a.l2_eps) : 1.f) * a.scale;
+            rk = a.l2norm ? 1.f / sqrtf(kk + a.l2_eps) : 1.f;
+            kq *= rq * rk;
+        } else {   // values whose squares or products FP32 does not hold: scaled by powers of two, as the chunks do
+            float mq = fmaxf(fmaxf(fabsf(qv.x), fabsf(qv.y)), fmaxf(fabsf(qv.z), fabsf(qv.w)));
+            float mk = fmaxf(fmaxf(fabsf(kv.x), fabsf(kv.y)), fmaxf(fabsf(kv.z), fabsf(kv.w)));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                mq = fmaxf(mq, __shfl_xor_sync(0xffffffffu, mq, o));
+                mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            }
+            const int eq = scale_exponent(mq, kRowTop), ek = scale_exponent(mk, kRowTop);
+            const float fq = pow2(eq), fk = pow2(ek);
+            qv = make_float4(qv.x * fq, qv.y * fq, qv.z * fq, qv.w * fq);
+            kv = make_float4(kv.x * fk, kv.y * fk, kv.z * fk, kv.w * fk);
+            qq = qv.x * qv.x + qv.y * qv.y + qv.z * qv.z + qv.w * qv.w;
+            kk = kv.x * kv.x + kv.y * kv.y + kv.z * kv.z + kv.w * kv.w;
+            kq = qv.x * kv.x + qv.y * kv.y + qv.z * kv.z + qv.w * kv.w;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                qq += __shfl_xor_sync(0xffffffffu, qq, o);
+                kk += __shfl_xor_sync(0xffffffffu, kk, o);
+                kq += __shfl_xor_sync(0xffffffffu, kq, o);
+            }
+            rq = (a.l2norm ? scaled_rsqrt(qq, eq, a.l2_eps) : pow2(-eq)) * a.scale;
+            rk = a.l2norm ? scaled_rsqrt(kk, ek, a.l2_eps) : pow2(-ek);
+            kq *= rq;
+            fu = rk;
+        }
+        if (warp == 0) *reinterpret_cast<float4*>(&sk[buf][4 * lane]) = make_float4(kv.x * rk, kv.y * rk, kv.z * rk, kv.w * rk);
+        if (warp == 1) *reinterpret_cast<float4*>(&sq[buf][4 * lane]) = make_float4(qv.x * rq, qv.y * rq, qv.z * rq, qv.w * rq);
         __syncthreads();
         float4 pk = make_float4(0.f, 0.f, 0.f, 0.f), pq = pk;
 #pragma unroll
@@ -323,8 +352,8 @@ __global__ void __launch_bounds__(kRecThreads) gdn_recurrent_kernel(const __grid
         }
         if (warp == 0 && sub == 0)
             *reinterpret_cast<uint2*>(a.out + (tok * a.HV + h) * kGdnDim + slice * SLICE + col) =
-                make_uint2(pack_bf16(fmaf(kq, u.x, pq.x), fmaf(kq, u.y, pq.y)),
-                           pack_bf16(fmaf(kq, u.z, pq.z), fmaf(kq, u.w, pq.w)));
+                make_uint2(pack_bf16(fmaf(kq, fu * u.x, pq.x), fmaf(kq, fu * u.y, pq.y)),
+                           pack_bf16(fmaf(kq, fu * u.z, pq.z), fmaf(kq, fu * u.w, pq.w)));
     }
 #pragma unroll
     for (int i = 0; i < kRows; ++i)

@@ -1,4 +1,4 @@
-// Device helpers shared by the gated-delta-rule kernels.
+// Helpers shared by the kernels of the layers around RMA attention.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -19,6 +19,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ float bf16_float(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// ---- powers of two ----
+__device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 0xffu) - 127; }
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| <= 126
+// the exponent of a scale that brings values of magnitude up to m into [.., 2^top): both it and its
+// negative are exponents of normal numbers, whatever m is
+__device__ __forceinline__ int scale_of_exponent(int e, int top) { return top - 1 - min(max(e, -110), 127); }
+__device__ __forceinline__ int scale_exponent(float m, int top) { return scale_of_exponent(exponent_of(m), top); }
+
+constexpr int kRowTop = 4;   // the largest value of a scaled row (of keys, queries) is below 2^kRowTop
+
+// What a row's values times 2^e have to be multiplied by to be x / sqrt(sum x^2 + eps), `sum` the sum of the scaled
+// squares.  One form keeps large rows from overflowing, the other rows far below eps from NaN.
+__device__ __forceinline__ float scaled_rsqrt(float sum, int e, float eps) {
+    const float f = pow2(e), inv = pow2(-e);
+    return e <= 60 || eps == 0.f ? 1.f / sqrtf(sum + eps * f * f) : inv / sqrtf(sum * inv * inv + eps);
+}
+
+// Whether sum x^2 (+ eps) may be used as it came out of FP32: no square has overflowed, and those that were flushed
+// do not count.  A NaN may not.
+__device__ __forceinline__ bool plain_sum(float v) { return v > 0x1p-90f && v < 0x1p110f; }
 
 // Tokens of sequence b, clamped to [0, n]; `report`: this thread sets the status bit.
 __device__ __forceinline__ int seq_len(const int32_t* lens, int b, int n, uint32_t* status, bool report) {

@@ -51,14 +51,6 @@ constexpr int kOffTLo = 1024, kOffP = 2 * kTile, kOffScal = 3 * kTile;
 // scales of T and P, and the bounds that the scan takes its scales from (see there)
 constexpr int kC1 = 0, kC2 = 64, kC3 = 128, kEC = 192, kTS = 193, kPS = 194, kBW = 196, kBT = 197, kBS = 198;
 
-// ---- powers of two ----
-__device__ __forceinline__ int exponent_of(float x) { return (int)((__float_as_uint(x) >> 23) & 0xffu) - 127; }
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| <= 126
-// the exponent of a scale that brings values of magnitude up to m into [.., 2^top): both it and its
-// negative are exponents of normal numbers, whatever m is
-__device__ __forceinline__ int scale_of_exponent(int e, int top) { return top - 1 - min(max(e, -110), 127); }
-__device__ __forceinline__ int scale_exponent(float m, int top) { return scale_of_exponent(exponent_of(m), top); }
-
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -125,7 +117,6 @@ __device__ __forceinline__ int p_lo_at(int row, int piece) {
 // launch 1
 // ---------------------------------------------------------------------------
 constexpr int kPrepThreads = 256;
-constexpr int kRowTop = 4;         // the largest value of a scaled row of K or Q is below 2^kRowTop
 constexpr int kHeadsAtOnce = 4;    // value heads whose gates are computed together, one per warp
 constexpr int kLd = kC + 4;        // row of a matrix that the tensor cores' fragments are read from
 
@@ -427,14 +418,8 @@ __device__ __forceinline__ void prep_item(const DeltaArgs& a, PrepSmem& s, int N
                 if (l8 == it) ssr = ss[it], sar = sa[it], mxr = mx[it];
             if (l8 < 4) {
                 const int m = l8 >> 1, row = (l8 & 1) * 32 + row0, e = scale_exponent(mxr, kRowTop);
-                const float f = pow2(e), inv = pow2(-e);
-                // 1 / sqrt(sum x^2 + eps) times the row's scale; the sum is of scaled values, so the one
-                // form keeps large rows from overflowing and the other rows far below eps from NaN
-                float r = inv;
-                if (a.l2norm) {
-                    if (e <= 60 || a.l2_eps == 0.f) r = 1.f / sqrtf(ssr + a.l2_eps * f * f);
-                    else r = inv / sqrtf(ssr * inv * inv + a.l2_eps);
-                }
+                const float inv = pow2(-e);
+                float r = a.l2norm ? scaled_rsqrt(ssr, e, a.l2_eps) : inv;
                 if (row >= valid) r = 0.f;
                 if (m) {
                     r *= a.scale;

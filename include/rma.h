@@ -464,9 +464,11 @@ RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qk
  * the SM count) run in chunks of 64, two launches on the stream (for few heads
  * and 32 chunks or more a memset and one cooperative launch of a block on every
  * SM, which waits until all SMs are free), shorter ones token by token.  The
- * chunks keep the state to about 2^-20 of its largest values, as FP32 sums do;
- * the outputs, before their rounding to BF16, to about 2^-20 of their terms and
- * 2^-30 of the largest of their column in the chunk.  After RMA_STATUS_TIMEOUT the
+ * chunks keep the state to about 2^-20 of its largest values, as FP32 sums do,
+ * and 2^-30 of the largest that the same value column had in the chunk (which
+ * counts where a state fades by more than that within 64 tokens); the outputs,
+ * before their rounding to BF16, to about 2^-20 of their terms and 2^-30 of the
+ * largest of their column in the chunk.  After RMA_STATUS_TIMEOUT the
  * delta state and outputs of the call are not valid. */
 RMA_API int rma_gdn_prefill(rma_gdn_state* st, int layer, int n_tok, const uint16_t* qkv,
                     const uint16_t* a, const uint16_t* b, int64_t ab_stride,

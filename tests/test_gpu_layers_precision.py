@@ -40,3 +40,60 @@ def test_block_outputs_are_of_fp32_arithmetic(batch, n, hk, hv, fresh):
     # sums of 128 terms and more in accumulators of 23 bits: at most 2^-16 of their absolute sum, in the updates and again here
     close(out, ref, 2.0 ** -15 * osize, "out")
     assert share_off(out, ref) <= 0.01
+
+
+# Keys, values and states far outside the range whose squares and products FP32 holds: (queries and keys, values, state)
+FAR = [(2.0 ** 70, 1.0, 1.0), (2.0 ** 100, 2.0 ** -50, 2.0 ** -70), (2.0 ** -80, 2.0 ** 40, 1.0), (2.0 ** -100, 1.0, 2.0 ** 60)]
+
+
+@pytest.mark.parametrize("n", [1, 5, 70])
+@pytest.mark.parametrize("k_scale,v_scale,s_scale", FAR)
+def test_normed_rows_of_any_magnitude(n, k_scale, v_scale, s_scale):
+    """l2_eps = 0, rows of every finite magnitude: the token form (alone and in a short block) and the chunks agree with
+    the oracle, whose squares have 64 bits."""
+    rma, _, _, x = delta_case(2, n, 2, 4, seed=310)
+    spread = 2.0 ** torch.randint(-4, 5, x["qkv"].shape, generator=torch.Generator().manual_seed(11)).float()
+    scale = torch.cat((torch.full((512,), k_scale), torch.full((512,), v_scale)))
+    x["qkv"] = (x["qkv"].float() * spread * scale).to(BF)
+    x["state"] = x["state"] * s_scale
+    d = {k: v.cuda() for k, v in x.items()}
+    st = rma.GdnState(rma.GdnConfig(batch=2, n_k_heads=2, n_v_heads=4, l2_eps=0.0))
+    st.delta[0].copy_(d["state"])
+    out = torch.empty(2, n, 4, 128, dtype=BF, device="cuda")
+    if n == 1:
+        rma.gdn_decode_step(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out)
+    else:
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, st.workspace(n))
+    ref, S, osize, size = delta_reference(x, 2, l2_eps=0.0)
+    # The bounds of the test above; value columns do not meet, so each is held to its own size.  In a chunk a column's
+    # factors are pairs of FP16 under one power of two: what bounds them comes to lie below 2^15, and the smallest step
+    # is 2^-24, an error of 2^-40 of that bound in each of the 64 factors of an output (2^-34 in all, |q| |k| scale < 1).
+    # The bound is a sum of absolute values where the column's largest is about its root: 16 times as large.  2^-30, of
+    # the largest up to this chunk, as the state hands it on: case four has a state of 2^60 that fades to 2^32 meanwhile.
+    chunks = n > 8
+    floor, sfloor = np.zeros_like(osize), 0.0
+    for lo in range(0, n if chunks else 0, 64):
+        floor[:, lo:lo + 64] = 2.0 ** -30 * osize[:, :lo + 64].max(1, keepdims=True)
+        sfloor = 2.0 ** -30 * np.maximum(np.abs(f64(x["state"])).max(-2, keepdims=True), size.max(-2, keepdims=True))
+    close(out, ref, 2.0 ** -15 * osize + floor + 2.0 ** -120, "out")
+    assert (np.abs(f64(st.delta[0]) - S) <= 2.0 ** -15 * size.max(-2, keepdims=True) + sfloor + 2.0 ** -120).all()
+
+
+@pytest.mark.parametrize("n", [1, 5, 70])
+def test_an_update_of_zero_adds_nothing_however_large_its_key(n):
+    """Without the norm, b = -inf: u is 0, and k.q, beyond FP32, multiplies it.  The output is the old state's."""
+    rma, _, _, x = delta_case(1, n, 1, 2, seed=311, l2norm=False)
+    x["qkv"][..., :256] = (x["qkv"][..., :256].float() * 2.0 ** 68).to(BF)
+    x["b"][:] = -float("inf")
+    x["state"] = x["state"] * 2.0 ** -10
+    d = {k: v.cuda() for k, v in x.items()}
+    st = rma.GdnState(rma.GdnConfig(n_k_heads=1, n_v_heads=2, qk_l2norm=False))
+    st.delta[0].copy_(d["state"])
+    out = torch.empty(1, n, 2, 128, dtype=BF, device="cuda")
+    if n == 1:
+        rma.gdn_decode_step(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out)
+    else:
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, st.workspace(n))
+    ref, S, osize, size = delta_reference(x, 1, l2norm=False)
+    close(out, ref, 2.0 ** -15 * osize, "out")
+    assert (np.abs(f64(st.delta[0]) - S) <= 2.0 ** -15 * size.max((-1, -2), keepdims=True)).all()
