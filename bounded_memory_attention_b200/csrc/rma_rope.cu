@@ -18,9 +18,7 @@
 // itself (its counter is its own).  Two FP32 values an instruction and one table for four groups gave 14.0 us
 // there but 5.5 us for the 512.
 
-#include <cuda_bf16.h>
-
-#include "rma_internal.cuh"
+#include "rma_gdn.cuh"
 
 namespace rma {
 namespace {
@@ -28,22 +26,16 @@ namespace {
 constexpr int kHeads = kQPerGroup + 1;   // of one group: its queries and its key
 constexpr int kRopeThreads = 32 * kHeads;
 
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-
-__device__ __forceinline__ float2 unpack(uint32_t v) {
-    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162*>(&v);
-    return __bfloat1622float2(h);
-}
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // Where pair p of a half-split rotation lies in the tables: a lane takes eight in a row, as two fours, and the
 // lanes' first fours lie side by side (eight in a row each put all lanes on four banks: 8-way conflicts, which
 // held 2,048 tokens to 20 us).
 __device__ __forceinline__ int at_pair(int p) { return ((p >> 2) & 1) * 64 + ((p >> 3) << 2) + (p & 3); }
+
+__device__ __forceinline__ void unpack8(const uint4& raw, float (&x)[8]) {
+    const float2 p0 = unpack_bf16(raw.x), p1 = unpack_bf16(raw.y), p2 = unpack_bf16(raw.z), p3 = unpack_bf16(raw.w);
+    x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
+    x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
+}
 
 template <int T>   // tokens of a CTA
 __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
@@ -92,17 +84,26 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __g
     for (int t = 0; t < T; ++t) {
         if (t >= count) break;
         float x[8];
-        {
-            const float2 p0 = unpack(raw[t].x), p1 = unpack(raw[t].y), p2 = unpack(raw[t].z), p3 = unpack(raw[t].w);
-            x[0] = p0.x; x[1] = p0.y; x[2] = p1.x; x[3] = p1.y;
-            x[4] = p2.x; x[5] = p2.y; x[6] = p3.x; x[7] = p3.y;
-        }
+        unpack8(raw[t], x);
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = 1.f / sqrtf(ss * (1.f / kHeadDim) + a.eps);
+        float mean = ss * (1.f / kHeadDim) + a.eps;
+        if (!plain_sum(mean)) {   // squares that FP32 does not hold: all values times a power of two, which r takes back
+            const float f = mean >= 1.f ? 0x1p-80f : 0x1p80f;
+            ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] *= f;
+                ss = fmaf(x[i], x[i], ss);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            mean = ss * (1.f / kHeadDim) + a.eps * f * f;
+        }
+        const float r = 1.f / sqrtf(mean);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = x[i] * r * w[i];
 
@@ -148,7 +149,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __g
             }
         }
         reinterpret_cast<uint4*>(dst + t * dst_stride)[lane] =
-            make_uint4(pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7]));
+            make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
     }
 }
 
@@ -159,16 +160,8 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
     // tokens of 4 groups, 42 MB: 17.3 us with one, 14.8 with two at 8 CTAs an SM, 15.7 with four at 5).
     const int64_t tokens = (int64_t)a.B * a.n;
     const bool many = tokens * a.G >= 4096;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((many ? (tokens + 1) / 2 : tokens) * a.G), 1, 1);
-    cfg.blockDim = dim3(kRopeThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<2>, a) : cudaLaunchKernelEx(&cfg, qk_norm_rope_kernel<1>, a);
+    const PdlLaunch l((unsigned)((many ? (tokens + 1) / 2 : tokens) * a.G), kRopeThreads, 0, stream);
+    return many ? cudaLaunchKernelEx(&l.cfg, qk_norm_rope_kernel<2>, a) : cudaLaunchKernelEx(&l.cfg, qk_norm_rope_kernel<1>, a);
 }
 
 }  // namespace rma

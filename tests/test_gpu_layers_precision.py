@@ -14,7 +14,7 @@ import torch
 
 import oracle
 from _gpu import lib  # noqa: F401
-from test_gpu_layers import BF, _device, close, delta_case, f64  # noqa: F401
+from test_gpu_layers import BF, _device, close, delta_case, f64, rope_case, rope_check  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,15 @@ def test_an_update_of_zero_adds_nothing_however_large_its_key(n):
     ref, S, osize, size = delta_reference(x, 1, l2norm=False)
     close(out, ref, 2.0 ** -15 * osize, "out")
     assert (np.abs(f64(st.delta[0]) - S) <= 2.0 ** -15 * size.max((-1, -2), keepdims=True)).all()
+
+
+@pytest.mark.parametrize("n", [3, 2050])
+@pytest.mark.parametrize("scale,eps", [(2.0 ** 70, 1e-6), (2.0 ** 110, 0.0), (2.0 ** -80, 0.0), (2.0 ** -110, 0.0), (2.0 ** -80, 1e-6),
+                                       (2.0 ** -60, 2.0 ** -120)])
+def test_rotated_rows_of_any_magnitude(n, scale, eps):
+    rma, st, q, k, w_q, w_k, f, q_out, k_out = rope_case(1, n, 2, 32, seed=320)
+    q, k = ((t.float() * scale).to(BF) for t in (q, k))
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").view(1, n)
+    rma.qk_norm_rope(st, 0, q, k, w_q, w_k, f, q_out, k_out, positions=pos, eps=eps)
+    p = pos.cpu().numpy()
+    rope_check(q, k, w_q, w_k, f, q_out, k_out, p, p, eps=float(np.float32(eps)))
