@@ -109,3 +109,39 @@ def test_rotated_rows_of_any_magnitude(n, scale, eps):
     rma.qk_norm_rope(st, 0, q, k, w_q, w_k, f, q_out, k_out, positions=pos, eps=eps)
     p = pos.cpu().numpy()
     rope_check(q, k, w_q, w_k, f, q_out, k_out, p, p, eps=float(np.float32(eps)))
+
+
+@pytest.mark.parametrize("where", ["a", "b", "q", "k", "v", "overflow"])
+@pytest.mark.parametrize("t", [66, 101, 127])
+def test_what_is_not_finite_is_seen_from_its_token_on(where, t):
+    """A NaN, or unnormed keys whose products exceed FP32, at token t of head 1's: every output of that head from there on
+    and its state are not finite; the tokens of earlier chunks, the other head and the other sequence keep their bits."""
+    rma, _, _, x = delta_case(2, 160, 2, 2, seed=330, l2norm=where != "overflow")
+    st = rma.GdnState(rma.GdnConfig(batch=2, n_k_heads=2, n_v_heads=2, qk_l2norm=where != "overflow"))
+
+    def call():
+        d = {k: v.cuda() for k, v in x.items()}
+        st.delta[0].copy_(d["state"])
+        out = torch.empty(2, 160, 2, 128, dtype=BF, device="cuda")
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, st.workspace(160))
+        return out, st.delta[0].clone()
+
+    want, want_state = call()
+    row = x["qkv"][1, t].view(6, 128)
+    if where in "ab":
+        x[where][1, t, 1] = float("nan")
+    elif where == "overflow":
+        x["qkv"][1, t - 1:t + 1, 384:512] = torch.full((128,), 2.0 ** 66, dtype=BF)
+    else:
+        row["qkv".index(where) * 2 + 1, 3] = float("nan")
+    out, state = call()
+    assert torch.equal(out[0], want[0]) and torch.equal(state[0], want_state[0])
+    assert torch.equal(out[1, :, 0], want[1, :, 0]) and torch.equal(state[1, 0], want_state[1, 0])
+    assert torch.equal(out[1, :64, 1], want[1, :64, 1])
+    lost = ~torch.isfinite(out[1, :, 1].float())
+    if where == "q":
+        assert lost[t].all()
+    else:
+        # (a NaN in v is in its own value column alone)
+        lost, bad = (lost[:, 3], ~torch.isfinite(state[1, 1, :, 3])) if where == "v" else (lost.all(-1), ~torch.isfinite(state[1, 1]))
+        assert lost[t:].all() and bad.all()
