@@ -442,7 +442,7 @@ RMA_API int rma_gdn_conv(rma_gdn_state* st, int layer, int n_tok, const uint16_t
  *   qkv      bf16 [batch][C]   (as rma_gdn_conv writes it: q heads, k heads, v heads)
  *   a, b     bf16 [batch][n_v_heads], consecutive sequences ab_stride elements apart
  *            (+inf and -inf are allowed: forget all, forget nothing; beta 1, 0)
- *   a_log, dt_bias  f32 [n_v_heads], finite
+ *   a_log, dt_bias  f32 [n_v_heads], finite, exp(a_log) a normal FP32 number
  *   out      bf16 [batch][n_v_heads][128]   (written; must not overlap an input)
  * qkv and out 16-byte aligned; ab_stride >= n_v_heads. */
 RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qkv,
@@ -457,9 +457,10 @@ RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qk
  *            hold, and their outputs are not written
  *   out      bf16 [batch][n_tok][n_v_heads][128]   (written; must not overlap an input)
  *   ws       workspace of rma_gdn_workspace_bytes(st, n_tok) bytes
- * n_tok >= 1 and batch * n_tok <= 2^24.  qkv of the tokens inside the lengths
- * must be finite: a NaN or infinity there spoils its sequence's outputs from up
- * to 63 tokens before it on, and the state.
+ * n_tok >= 1 and batch * n_tok <= 2^24.  Inside the lengths qkv must be finite,
+ * a and b no NaN, and with l2_eps == 0 no row of q or k all zeros (its norm is
+ * 0 / 0): such a token spoils the outputs of the heads that read it from up to
+ * 63 tokens before it on, and their state (token by token only from it on).
  * Blocks of 13 tokens and more (9 and more where 4 batch * n_v_heads exceeds
  * the SM count) run in chunks of 64, two launches on the stream (for few heads
  * and 32 chunks or more a memset and one cooperative launch of a block on every

@@ -145,3 +145,22 @@ def test_what_is_not_finite_is_seen_from_its_token_on(where, t):
         # (a NaN in v is in its own value column alone)
         lost, bad = (lost[:, 3], ~torch.isfinite(state[1, 1, :, 3])) if where == "v" else (lost.all(-1), ~torch.isfinite(state[1, 1]))
         assert lost[t:].all() and bad.all()
+
+
+@pytest.mark.parametrize("what", ["a", "b", "zero key"])
+def test_how_far_back_a_chunk_is_spoilt(what):
+    """The reach that the header states: of a NaN gate, or of a key of zeros without eps, no token before the chunk's first
+    (at most 63 before it) is touched, in a block of chunks, and none before the token itself in a short block."""
+    for n, t, first in ((130, 100, 64), (6, 4, 4)):
+        rma, _, _, x = delta_case(1, n, 1, 1, seed=340)
+        st = rma.GdnState(rma.GdnConfig(n_k_heads=1, n_v_heads=1, l2_eps=0.0))
+        if what == "zero key":
+            x["qkv"][0, t, 128:256] = 0
+        else:
+            x[what][0, t] = float("nan")
+        d = {k: v.cuda() for k, v in x.items()}
+        st.delta[0].copy_(d["state"])
+        out = torch.empty(1, n, 1, 128, dtype=BF, device="cuda")
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, st.workspace(n))
+        fine = torch.isfinite(out.float()).flatten(2).all(-1)[0]
+        assert fine[:first].all() and not fine[t:].any() and not torch.isfinite(st.delta).any()
