@@ -71,7 +71,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "rma_admit_impl.cuh"
 #include "rma_internal.cuh"
@@ -970,29 +969,11 @@ __global__ void __launch_bounds__(kCopyThreads) prefill_admit_copy_kernel(const 
 
 // ---- host side: tensor maps through the driver entry point ----
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // 3-D BF16 tensor [d2][d1][256] with the given strides (bytes) for dims 1 and 2,
 // box (64, box1, box2), 128-byte swizzle, zero fill outside the tensor.
 bool make_map(CUtensorMap* m, const void* base, uint64_t d1, uint64_t d2, uint64_t stride1, uint64_t stride2,
               uint32_t box1, uint32_t box2) {
-    EncodeTiledFn fn = encode_fn();
+    TensorMapEncodeFn fn = tensor_map_encode();
     if (!fn) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)d1, (cuuint64_t)d2};
     const cuuint64_t strides[2] = {(cuuint64_t)stride1, (cuuint64_t)stride2};
@@ -1007,7 +988,7 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t d1, uint64_t d2, uint64
 // x 8 tokens (one softmax warp's 32 rows), 128-byte swizzle (the rows' 16-byte pieces permuted by
 // row within 8-row groups).
 bool make_ws_map(CUtensorMap* m, void* ws, int HQ, int n, int B) {
-    EncodeTiledFn fn = encode_fn();
+    TensorMapEncodeFn fn = tensor_map_encode();
     if (!fn) return false;
     const uint64_t row = (uint64_t)kHeadDim * 4;
     const cuuint64_t dims[5] = {(cuuint64_t)kHeadDim, (cuuint64_t)HQ, (cuuint64_t)n, (cuuint64_t)B, 2};
