@@ -685,7 +685,7 @@ static_assert(kScanSmem <= 227 * 1024, "shared memory per CTA");
 //   S   [0, 128)    per half: S0 as hi, lo (32 + 32); then the state's increment (64, FP32)
 //   W   [128, 192)  per half: W (32); then the scaled U as hi, lo (16 + 16)
 //   X   [192, 256)  per half: X as hi, lo (16 + 16)
-//   U   [256, 320)  U by the first half's X; then per half U as hi, lo (16 + 16)
+//   U   [256, 320)  U by the first half's X; then U as hi, lo, hi, lo (8 each, of 16 tokens) per half
 //   Q S0 [320, 384),  P U [384, 448) by the first half's U
 //   [448, 480) U of the second half's tokens by their own X,  [480, 512) their P U by their own U
 constexpr uint32_t kTmS = 0, kTmW = 128, kTmX = 192, kTmU = 256, kTmCols = 512;
@@ -766,11 +766,6 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     f2 r;
     asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
@@ -797,8 +792,23 @@ __device__ __forceinline__ void lds4(const float* p, f2& a, f2& b) {
     b = v.y;
 }
 
+// ptx::mbar_wait_warp in less code, of which the scan has twenty copies: it gives up without setting the status, which is
+// set once, at the CTA's end (8,192 tokens of 32 heads: 354 us, 395 with the longer form; the instruction caches).
+__device__ __forceinline__ bool scan_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    const long long t0 = clock64();
+    bool ok = true;
+    while (!ptx::mbar_try_wait(bar, parity)) {
+        if (*abort || clock64() - t0 > ptx::kWaitLimitCycles) {
+            *abort = 1;
+            ok = false;
+            break;
+        }
+    }
+    return __all_sync(0xffffffffu, ok);
+}
+
 // Wait, bounded as the waits on barriers are, until another CTA has set the flag.  By a whole warp, with one verdict.
-__device__ __forceinline__ bool item_ready(const uint32_t* flag, volatile int* abort, uint32_t* status) {
+__device__ __forceinline__ bool item_ready(const uint32_t* flag, volatile int* abort) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) {
         const long long t0 = clock64();
@@ -808,7 +818,6 @@ __device__ __forceinline__ bool item_ready(const uint32_t* flag, volatile int* a
             if (v != 0) break;
             if (*abort || clock64() - t0 > ptx::kWaitLimitCycles) {
                 *abort = 1;
-                atomicOr(status, (unsigned)RMA_STATUS_TIMEOUT);
                 ok = false;
                 break;
             }
@@ -892,10 +901,10 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             int issued = 0;
             for (int c = 0; c < nc; ++c) {
                 const int st = c % kStages;
-                if (c >= kStages && !ptx::mbar_wait_warp(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag, a.status)) break;
+                if (c >= kStages && !scan_wait(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag)) break;
                 // the state and the first chunk come first: they are what the start waits for
-                if (c == 1 && !ptx::mbar_wait_warp(&bars[kbS], 0, abort_flag, a.status)) break;
-                if (ready && !item_ready(ready + ((int64_t)c * a.B + b) * a.HK + kh, abort_flag, a.status)) break;
+                if (c == 1 && !scan_wait(&bars[kbS], 0, abort_flag)) break;
+                if (ready && !item_ready(ready + ((int64_t)c * a.B + b) * a.HK + kh, abort_flag)) break;
                 issued = c + 1;
                 uint8_t* stage = smem + st * kStageBytes;
                 if (lane == 0) {
@@ -928,7 +937,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 // columns).  16 values of the rows of an image are 32 bytes: 2 in the address field
                 const uint32_t dk = (kb >> 4) | (1u << 16), dt = (tb >> 4) | (1u << 16), dd = (kb >> 4) | ((uint32_t)(kTile >> 4) << 16);
                 auto wait = [&](int bar, int phase) {
-                    const bool there = ptx::mbar_wait_warp(&bars[bar], phase & 1, abort_flag, a.status);
+                    const bool there = scan_wait(&bars[bar], phase & 1, abort_flag);
                     ptx::tc_fence_after();
                     return there;
                 };
@@ -984,16 +993,16 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 // P U, as U
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    const uint32_t u = kTmU + 8 * ks, p = dt + kP + 2 * ks;
+                    const uint32_t u = kTmU + 16 * ks, p = dt + kP + 2 * ks;
                     product<kAccP>(u, p, ks > 0, go);
-                    product<kAccP>(u + 16, p, true, go);
+                    product<kAccP>(u + 8, p, true, go);
                     product<kAccP>(u, dt + 4 + 2 * ks, true, go);
                 }
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    const uint32_t u = kTmU + 32 + 8 * ks, p = dt + kP + kHalfRows + 4 + 2 * ks;
+                    const uint32_t u = kTmU + 32 + 16 * ks, p = dt + kP + kHalfRows + 4 + 2 * ks;
                     product<kAccP2>(u, p, ks > 0, go);
-                    product<kAccP2>(u + 16, p, true, go);
+                    product<kAccP2>(u + 8, p, true, go);
                     product<kAccP2>(u, dt + kP + 4 + 2 * ks, true, go);
                 }
                 ptx::mma_commit1(&bars[kbPDone], go);
@@ -1015,10 +1024,10 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             uint8_t* stage = smem + st * kStageBytes;
             const float* scal = reinterpret_cast<const float*>(stage + kStageTP + kOffScal);
             const int left = len - c * kC;
-            ok = ptx::mbar_wait_warp(&bars[kbFull + st], (c / kStages) & 1, abort_flag, a.status) && ok;
-            ok = ptx::mbar_wait_warp(&bars[kbU], c & 1, abort_flag, a.status) && ok;   // the scales
+            ok = scan_wait(&bars[kbFull + st], (c / kStages) & 1, abort_flag) && ok;
+            ok = scan_wait(&bars[kbU], c & 1, abort_flag) && ok;   // the scales
             const float inv_p = scal[kPS];
-            ok = ptx::mbar_wait_warp(&bars[kbPDone], c & 1, abort_flag, a.status) && ok;
+            ok = scan_wait(&bars[kbPDone], c & 1, abort_flag) && ok;
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int hl = 0; hl < 2; ++hl) {            // 16 columns
@@ -1162,7 +1171,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             const float* one = reinterpret_cast<const float*>(smem + st * kStageBytes + kStageTP + kOffScal);
             const float* scal = one + 32 * wg;   // this half's tokens
             // while W is computed: the bounds and the scales
-            ok = ptx::mbar_wait_warp(&bars[kbS + (wg ^ 1)], c & 1, abort_flag, a.status) && ok;
+            ok = scan_wait(&bars[kbS + (wg ^ 1)], c & 1, abort_flag) && ok;
             take(smax, vmax);
             const float inv_s = pow2(-es);
             smax *= inv_s;
@@ -1182,7 +1191,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             }
             // X
             // (an abandoned CTA goes on through its barriers, on values that nobody uses)
-            ok = ptx::mbar_wait_warp(&bars[kbWDone], c & 1, abort_flag, a.status) && ok;
+            ok = scan_wait(&bars[kbWDone], c & 1, abort_flag) && ok;
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmW + 32 * wg, x);
             ptx::tmem_wait_ld();
@@ -1202,51 +1211,50 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 signal(kbX);
             }
             // U, and U scaled for the state
-            ok = ptx::mbar_wait_warp(&bars[kbUDone + wg], c & 1, abort_flag, a.status) && ok;
+            ok = scan_wait(&bars[kbUDone + wg], c & 1, abort_flag) && ok;
             ptx::tc_fence_after();
-            ptx::tmem_ld32(tl + kTmU + 32 * wg, x);
-            if (wg == 1) {   // by both halves' X
-                uint32_t y[32];
-                ptx::tmem_ld32(tl + kAcc[kAccU2].column, y);
-                ptx::tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float2 z = unpack2(add2(pack2(x[2 * i], x[2 * i + 1]), pack2(y[2 * i], y[2 * i + 1])));
-                    x[2 * i] = __float_as_uint(z.x);
-                    x[2 * i + 1] = __float_as_uint(z.y);
-                }
-            } else {
-                ptx::tmem_wait_ld();
-            }
             {
                 const f2 cu2 = pack2(cu, cu), cd2 = pack2(cd, cd);
-                uint32_t hi[16], lo[16];
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t u[16], hi[8], lo[8];
+                    ptx::tmem_ld16(tl + kTmU + 32 * wg + 16 * p, u);
+                    if (wg == 1) {   // by both halves' X
+                        uint32_t y[16];
+                        ptx::tmem_ld16(tl + kAcc[kAccU2].column + 16 * p, y);
+                        ptx::tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    f2 c3[2];
-                    lds4(scal + kC3 + 2 * i, c3[0], c3[1]);
+                        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) + __uint_as_float(y[i]));
+                    } else {
+                        ptx::tmem_wait_ld();
+                    }
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        split2(mul2(pack2(x[2 * (i + j)], x[2 * (i + j) + 1]), mul2(c3[j], cd2)), hi[i + j], lo[i + j]);
+                    for (int i = 0; i < 8; i += 2) {
+                        f2 c3[2];
+                        lds4(scal + kC3 + 16 * p + 2 * i, c3[0], c3[1]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            split2(mul2(pack2(u[2 * (i + j)], u[2 * (i + j) + 1]), mul2(c3[j], cd2)), hi[i + j], lo[i + j]);
+                    }
+                    ptx::tmem_st8(tl + kTmW + 32 * wg + 8 * p, hi);
+                    ptx::tmem_st8(tl + kTmW + 32 * wg + 16 + 8 * p, lo);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) split2(mul2(pack2(u[2 * i], u[2 * i + 1]), cu2), hi[i], lo[i]);
+                    ptx::tmem_st8(tl + kTmU + 32 * wg + 16 * p, hi);
+                    ptx::tmem_st8(tl + kTmU + 32 * wg + 16 * p + 8, lo);
                 }
-                ptx::tmem_st16(tl + kTmW + 32 * wg, hi);
-                ptx::tmem_st16(tl + kTmW + 32 * wg + 16, lo);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) split2(mul2(pack2(x[2 * i], x[2 * i + 1]), cu2), hi[i], lo[i]);
-                ptx::tmem_st16(tl + kTmU + 32 * wg, hi);
-                ptx::tmem_st16(tl + kTmU + 32 * wg + 16, lo);
                 signal(kbU);
             }
             if (lane == 0) ptx::mbar_arrive(&bars[kbEmpty + st]);   // (the output warps wait for the products)
           }
             // while the increment is computed: the next chunk's V
             if (c + 1 < nc) {
-                ok = ptx::mbar_wait_warp(&bars[kbFull + (c + 1) % kStages], ((c + 1) / kStages) & 1, abort_flag, a.status) && ok;
+                ok = scan_wait(&bars[kbFull + (c + 1) % kStages], ((c + 1) / kStages) & 1, abort_flag) && ok;
                 vmax = get_v(c + 1);
             }
             // the state
             if (c >= 0) {
-                ok = ptx::mbar_wait_warp(&bars[kbDDone], c & 1, abort_flag, a.status) && ok;
+                ok = scan_wait(&bars[kbDDone], c & 1, abort_flag) && ok;
                 ptx::tc_fence_after();
                 es = es1;
                 const f2 k2 = pack2(ck, ck);
@@ -1291,6 +1299,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == kWarpMma) ptx::tmem_dealloc1(tmem, kTmCols);
+    if (tid == 0 && *abort_flag) atomicOr(a.status, (unsigned)RMA_STATUS_TIMEOUT);
 }
 
 __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_constant__ DeltaArgs a,

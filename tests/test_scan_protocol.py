@@ -38,7 +38,7 @@ def test_the_kernel_hands_over_with_the_state():
     """The scan arrives on no named barrier without waiting there, and a half waits for the other's state, bounded."""
     src = open(SOURCE).read()
     assert "named_bar_arrive" not in src
-    assert "mbar_wait_warp(&bars[kbS + (wg ^ 1)], c & 1, abort_flag" in src
+    assert "scan_wait(&bars[kbS + (wg ^ 1)], c & 1, abort_flag)" in src
 
 
 def test_an_abandoned_cta_stores_no_outputs():
