@@ -20,8 +20,16 @@ _current_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _call(function, name: str, index: int, stream, *args) -> None:
-    """`function(*args, stream)` with device `index` current; its error raised."""
+def _int32(value: int, name: str) -> int:
+    """`value`, which ctypes would otherwise cut to its low 32 bits."""
+    if not -1 << 31 <= value < 1 << 31:
+        raise ValueError(f"{name} is beyond 32 bits: {value}")
+    return value
+
+
+def _call(function, name: str, index: int, stream, handle, layer, *args) -> None:
+    """`function(handle, layer, *args, stream)` with device `index` current; its error raised."""
+    args = (handle, _int32(layer, "layer"), *args)
     if _current_device() == index:
         code = function(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
@@ -122,8 +130,8 @@ class GdnConfig:
     scale: float = 128 ** -0.5
 
     def _c(self) -> _GdnConfig:
-        return _GdnConfig(self.batch, self.n_layers, self.n_k_heads, self.n_v_heads, self.head_dim,
-                          self.conv_width, int(self.qk_l2norm), self.l2_eps, self.scale)
+        sizes = (_int32(getattr(self, f), f) for f in ("batch", "n_layers", "n_k_heads", "n_v_heads", "head_dim", "conv_width"))
+        return _GdnConfig(*sizes, _int32(int(self.qk_l2norm), "qk_l2norm"), self.l2_eps, self.scale)
 
     @property
     def channels(self) -> int:
@@ -186,7 +194,7 @@ class GdnState:
 
     def workspace_bytes(self, n_tok: int) -> int:
         out = ctypes.c_size_t()
-        _check(lib.rma_gdn_workspace_bytes(self._h, int(n_tok), ctypes.byref(out)), "rma_gdn_workspace_bytes")
+        _check(lib.rma_gdn_workspace_bytes(self._h, _int32(int(n_tok), "n_tok"), ctypes.byref(out)), "rma_gdn_workspace_bytes")
         return int(out.value)
 
     def workspace(self, n_tok: int) -> torch.Tensor:
