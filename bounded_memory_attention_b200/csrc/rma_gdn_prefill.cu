@@ -63,6 +63,8 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     lo = half2_bits(a - f.x, b - f.y);
 }
 
+// 2^x to 2^-22: as near as the pairs that its results are multiplied into, and one instruction.  (Results below 2^-126,
+// flushed to 0, are decays of what has faded.)
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
@@ -120,7 +122,7 @@ constexpr int kPrepThreads = 256;
 constexpr int kHeadsAtOnce = 4;    // value heads whose gates are computed together, one per warp
 constexpr int kLd = kC + 4;        // row of a matrix that the tensor cores' fragments are read from
 
-// Measured on one B200: 80 us for 8,192 tokens of 16 key and 32 value heads, 2,048 CTAs.  It issues in half of
+// Measured on one B200: 89 us for 8,192 tokens of 16 key and 32 value heads, 2,048 CTAs.  It issues in half of
 // the cycles, 25,000 warp instructions a CTA; what stalls it are the group's barriers between the short phases
 // (24 warps an SM, which registers and shared memory both limit) and shared memory, half of its wavefronts.
 // K K^T and Q K^T by tcgen05 instead of mma.sync took the same time: the products are a small part.  So did fewer
@@ -653,15 +655,14 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // launch 2
 //
-// Bound by latency: the chunks of a head follow one another, 2.3 us each (4,300 cycles: the state's update and
-// split 1,050, wait for W 870, X 460, wait for U 520, U 580, V and the increment 750), and a CTA starts and
-// ends in 8 us.  Measured on one B200: 300 us for 8,192 tokens of one sequence (32 CTAs), 35 us for 8 x 256
+// Bound by latency: the chunks of a head follow one another, 2.6 us each (4,900 cycles: the state's update and
+// split 1,000, wait for W 500, X 680, wait for U 550, its splits 900, V and the increment 1,050), and a CTA starts and
+// ends in 8 us.  Measured on one B200: 335 us for 8,192 tokens of one sequence (32 CTAs), 37 us for 8 x 256
 // (256 CTAs on 148 SMs).  What shortened the chain: products issued by one elected lane of a converged
-// warp (17 to 32 cycles an instruction; from a branch of one lane 103), the state's two halves half a phase
-// apart, scales from bounds that the first launch computes instead of maxima over the chunk, outputs left to
-// warps of their own, and registers moved to the warps that hold the state (other splits: 3% and 6% slower).
-// CTAs that take several heads in turn were no faster; the loops stand once each since the instruction
-// cache misses on 18% of the requests as it is.
+// warp (39 cycles an instruction; from a branch of one lane 103), scales from bounds that the first launch computes
+// instead of maxima over the chunk, outputs left to warps of their own, registers moved to the warps that hold the
+// state (other splits: 3% and 6% slower), and little code: one copy of each loop, short waits, since the instruction
+// cache misses on 10% of the requests as it is.  CTAs that take several heads in turn were no faster.
 // ---------------------------------------------------------------------------
 constexpr int kStageTP = kKQBytes;                        // offsets in a stage
 constexpr int kStageV = (kKQBytes + kTPBytes + 1023) / 1024 * 1024;   // V rows; then, in their place, the outputs
@@ -1312,8 +1313,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
 // items at a time of launch 1, chunk by chunk.  A finished item sets its flag, and a head's loads wait for it.  The
 // launch is cooperative, so that all CTAs are there, and those that are waited for do not wait themselves.
 //
-// Measured on one B200, 16 key and 32 value heads: 333 us for 8,192 tokens (386 in two launches), 103 (108) for 2,048,
-// 64 (62) for 1,024; two sequences of 4,096 tokens 203 (242).
+// Measured on one B200, 16 key and 32 value heads: 355 us for 8,192 tokens (424 in two launches), 108 (116) for 2,048;
+// two sequences of 4,096 tokens 206 (260).
 // ---------------------------------------------------------------------------
 constexpr int kPrepSlot = (sizeof(PrepSmem) + 1023) / 1024 * 1024;
 static_assert(2 * kPrepThreads == kScanThreads && 2 * kPrepSlot + 1024 <= kScanSmem, "two items in a CTA of the scan's size");
@@ -1369,10 +1370,13 @@ size_t gdn_prefill_workspace_bytes(const rma_gdn_config& c, int n) {
 }
 
 // Heads on at most half of the multiprocessors, 32 chunks or more, and the others keep ahead of the heads: an item
-// with two value heads takes 12 us, two items at a time a CTA, a chunk of the scan 2.3 us.
+// with two value heads takes 12 us, two items at a time a CTA, a chunk of the scan 2.6 us.  And more items than launch 1
+// runs at once, three an SM, since with fewer it is over in the time of one: 2,048 tokens of 8 and 16 heads (256 items)
+// 104 us here, 100 in two launches, 8,192 of 2 and 4 (256) 344 and 342; 2,048 of 16 and 16 (512) 102 and 108, 8,192 of 4
+// and 4 (512) 342 and 352.
 static bool in_one_launch(const DeltaArgs& a, int NC) {
     const int heads = a.B * a.HV, rest = a.sm_count - heads;
-    return NC >= 32 && rest >= heads && 5ll * a.B * a.HK * ((a.HV / a.HK + 1) / 2) <= 2 * rest;
+    return NC >= 32 && (int64_t)NC * a.B * a.HK > 3 * a.sm_count && rest >= heads && 5ll * a.B * a.HK * ((a.HV / a.HK + 1) / 2) <= 2 * rest;
 }
 
 cudaError_t launch_gdn_prefill(const DeltaArgs& a, cudaStream_t stream) {

@@ -462,9 +462,9 @@ RMA_API int rma_gdn_decode_step(rma_gdn_state* st, int layer, const uint16_t* qk
  * 0 / 0): such a token spoils the outputs of the heads that read it from up to
  * 63 tokens before it on, and their state (token by token only from it on).
  * Blocks of 13 tokens and more (9 and more where 4 batch * n_v_heads exceeds
- * the SM count) run in chunks of 64, two launches on the stream (for few heads
- * and 32 chunks or more a memset and one cooperative launch of a block on every
- * SM, which waits until all SMs are free), shorter ones token by token.  The
+ * the SM count) run in chunks of 64, two launches on the stream (where few heads
+ * have 32 chunks and many more a memset and one cooperative launch of a block on
+ * every SM, which waits until all SMs are free), shorter ones token by token.  The
  * chunks keep the state to about 2^-20 of its largest values, as FP32 sums do,
  * and 2^-30 of the largest that the same value column had in the chunk (which
  * counts where a state fades by more than that within 64 tokens); the outputs,

@@ -185,3 +185,77 @@ def test_random_shapes_through_a_delta_layer(seed):
     assert (f64(out)[past] == 7.0).all()
     assert torch.equal(st.conv[1 - layer], other[0]) and torch.equal(st.delta[1 - layer], other[1])
     assert rma.gdn_get_status(st) == 0
+
+
+@pytest.mark.parametrize("batch,hk,hv,n,lens", [(1, 16, 16, 2049, None), (2, 7, 7, 2070, [2070, 1999]), (3, 4, 8, 2500, [2500, 0, 77]),
+                                                (1, 4, 12, 7200, None)])
+def test_blocks_of_few_heads_in_one_launch(batch, hk, hv, n, lens):
+    """More items than the first launch runs at once, few heads: one cooperative launch, whatever the workspace held, the
+    same bits every time and the bits of the two launches that a sequence alone takes."""
+    rma, st, d, x = delta_case(batch, n, hk, hv, seed=600 + batch)
+    assert -(-n // 64) * batch * hk > 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    ln = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for b, m in enumerate(lens or []):
+        d["qkv"][b, m:] = float("nan")
+    ws, first = st.workspace(n), None
+    for fill in (1, 255, 0, None):
+        out = torch.full((batch, n, hv, 128), 7.0, dtype=BF, device="cuda")
+        if fill is not None:
+            ws.fill_(fill)
+        st.delta[0].copy_(d["state"])
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, ws, lens=ln)
+        first = first or (out.clone(), st.delta.clone())
+        assert torch.equal(out, first[0]) and torch.equal(st.delta, first[1])
+    past, _ = fp32_check(out, st.delta[0], x, hk, True, lens=lens)
+    assert (f64(out)[past] == 7.0).all() and rma.gdn_get_status(st) == 0
+    # one key head's value heads alone go in two launches
+    r = hv // hk
+    few = rma.GdnState(rma.GdnConfig(batch=batch, n_k_heads=1, n_v_heads=r))
+    few.delta[0].copy_(d["state"][:, -r:])
+    q = torch.cat((d["qkv"][..., (hk - 1) * 128:hk * 128], d["qkv"][..., (2 * hk - 1) * 128:2 * hk * 128], d["qkv"][..., -r * 128:]), -1)
+    one = torch.full((batch, n, r, 128), 7.0, dtype=BF, device="cuda")
+    rma.gdn_prefill(few, 0, q.contiguous(), d["a"][..., -r:].contiguous(), d["b"][..., -r:].contiguous(), d["a_log"][-r:].contiguous(),
+                    d["dt_bias"][-r:].contiguous(), one, few.workspace(n), lens=ln)
+    assert torch.equal(one, out[:, :, -r:]) and torch.equal(few.delta[0], st.delta[0, :, -r:])
+
+
+def test_two_cooperative_launches_at_once_and_replayed():
+    """Two such blocks of two states on two streams at once, then both replayed from graphs at once, among calls of the other
+    kinds: the bits of the calls alone."""
+    rma, sides = lib(), []
+    for side in range(2):
+        _, st, d, _ = delta_case(1, 2048, 16, 16, seed=610 + side)
+        w = si.f32_normal((st.cfg.channels, 4), 612 + side, std=0.5).cuda()
+        ws, out = st.workspace(2048), torch.empty(1, 2048, 16, 128, dtype=BF, device="cuda")
+        y, one = torch.empty_like(d["qkv"]), torch.empty(1, 16, 128, dtype=BF, device="cuda")
+
+        def call(st=st, d=d, w=w, ws=ws, out=out, y=y, one=one):
+            rma.gdn_conv(st, 0, d["qkv"], w, y)
+            rma.gdn_prefill(st, 0, y, d["a"], d["b"], d["a_log"], d["dt_bias"], out, ws)
+            rma.gdn_decode_step(st, 0, y[:, 99].contiguous(), d["a"][:, 99], d["b"][:, 99], d["a_log"], d["dt_bias"], one)
+
+        call()
+        torch.cuda.synchronize()
+        sides.append((st, d, out, one, (out.clone(), one.clone(), st.buffer.clone()), call, torch.cuda.Stream(), torch.cuda.CUDAGraph()))
+
+    def at_once(run):
+        for st, d, out, *_ in sides:
+            st.conv.zero_()
+            st.delta[0].copy_(d["state"])
+            out.fill_(3.0)
+        torch.cuda.synchronize()
+        for side in sides:
+            with torch.cuda.stream(side[6]):
+                run(side)
+        torch.cuda.synchronize()
+        for st, d, out, one, want, *_ in sides:
+            assert torch.equal(out, want[0]) and torch.equal(one, want[1]) and torch.equal(st.buffer, want[2])
+            assert rma.gdn_get_status(st) == 0
+
+    for _ in range(3):
+        at_once(lambda side: side[5]())
+    for side in sides:
+        with torch.cuda.graph(side[7], stream=side[6]):
+            side[5]()
+    for _ in range(3):
+        at_once(lambda side: side[7].replay())
