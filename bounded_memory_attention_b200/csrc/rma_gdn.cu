@@ -15,10 +15,11 @@ namespace {
 // sequences' loads in flight.  The state is read by the first tile only and written by the same
 // threads, after their reads.
 //
-// Measured on one B200, 8,192 channels: 4 ragged prompts of up to 2,048 tokens (201 MB) 44.9 us, 4.5 TB/s;
-// 512 single tokens (67 MB) 14.0 us, 4.8 TB/s.  Blocks issue in 69% of the cycles and their special-function
-// pipe is as busy, so eight CTAs of an SM are needed to cover the loads.  Slower there: tiles of 16 or 64 tokens
-// (47.6, 46.3), two or eight rows on their way (48, 62), 16 rows through shared memory (50).
+// Measured on one B200, 8,192 channels: 4 ragged prompts of up to 2,048 tokens, 7,202 in all (237 MB), 44.8 us,
+// 5.3 TB/s; 512 single tokens (67 MB) 14.0 us, 4.8 TB/s: 2,048 CTAs, of which 9 fit an SM (110 registers), 1.5 waves.
+// Blocks issue in 69% of the cycles and their special-function pipe is as busy, so eight CTAs of an SM are needed to
+// cover the loads (at 64 registers, of which one is spilled).  Slower there: tiles of 16 or 64 tokens (47.6, 46.3), two
+// or eight rows on their way (48, 62), 16 rows through shared memory (50).
 // ---------------------------------------------------------------------------
 constexpr int kConvThreads = 128;
 constexpr int kTokenThreads = 64;
@@ -227,7 +228,7 @@ __global__ void __launch_bounds__(kTokenThreads) gdn_conv_token_kernel(const __g
 // shuffles and one exchange in shared memory.  Everything is FP32.
 //
 // Measured on one B200, one token: 3.1 us for one sequence of 32 value heads (4 CTAs a head), 7.6 us for 37
-// of 6 heads (29 MB, 3.8 TB/s), 317 us for 512 of 32 heads (2.16 GB, 6.8 TB/s).
+// of 6 heads (29 MB, 3.8 TB/s; 888 CTAs, of which 4 fit an SM: 1.5 waves), 317 us for 512 of 32 heads (2.16 GB, 6.8 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kRecThreads = 256;
 constexpr int kRecWarps = kRecThreads / 32;

@@ -215,7 +215,7 @@ struct DeltaArgs {
 cudaError_t launch_gdn_recurrent(const DeltaArgs& a, cudaStream_t stream);
 // Blocks shorter than this go token by token, and up to kGdnChunkedFromFew where few heads leave the token form
 // its four CTAs a head.  Measured with 16 key and 32 value heads, token form / chunks: 1 sequence of 12 tokens
-// 15.6 / 17.0 us, of 16 20.2 / 16.8; 4 of 8 24.8 / 26.1; 256 of 8 566 / 570 us, of 12 804 / 571.
+// 16.4 / 17.1 us, of 13 17.6 / 17.0; 4 of 8 25.2 / 25.6, of 9 28.0 / 25.6; 256 of 8 571 / 593 us, of 9 633 / 594.
 constexpr int kGdnChunkedFrom = 9, kGdnChunkedFromFew = 13;
 cudaError_t launch_gdn_prefill(const DeltaArgs& a, cudaStream_t stream);
 size_t gdn_prefill_workspace_bytes(const rma_gdn_config& c, int n);

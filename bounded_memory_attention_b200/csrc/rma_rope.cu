@@ -13,7 +13,8 @@
 // eight values do not have one side (rotary_dim / 2 not a multiple of 8).
 //
 // Measured on one B200, 4 groups: 1.9 us for one token, 5.1 us for 512 sequences of one token (64 values
-// rotated), 14.8 us for 8 x 256 tokens with all 256 rotated (42 MB, 2.8 TB/s).  The last is 3.5 waves of short
+// rotated; 2,048 CTAs, of which 8 fit an SM: 1.7 waves), 15.2 us for 8 x 256 tokens with all 256 rotated (42 MB,
+// 2.8 TB/s; 14.8 before the sums were checked for what FP32 holds).  The last is 3.5 waves of short
 // CTAs that issue in 78% of the cycles, about a third of it for the angles, which every group computes for
 // itself (its counter is its own).  Two FP32 values an instruction and one table for four groups gave 14.0 us
 // there but 5.5 us for the 512.
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __g
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t stream) {
     // Few tokens: one a CTA, as many CTAs as there can be.  Many: two, whose loads are both in flight (8 x 256
-    // tokens of 4 groups, 42 MB: 17.3 us with one, 14.8 with two at 8 CTAs an SM, 15.7 with four at 5).
+    // tokens of 4 groups, 42 MB: 17.7 us with one, 15.2 with two at 8 CTAs an SM, 15.5 at 7).
     const int64_t tokens = (int64_t)a.B * a.n;
     const bool many = tokens * a.G >= 4096;
     const PdlLaunch l((unsigned)((many ? (tokens + 1) / 2 : tokens) * a.G), kRopeThreads, 0, stream);
