@@ -31,10 +31,10 @@ __device__ __forceinline__ int scale_exponent(float m, int top) { return scale_o
 constexpr int kRowTop = 4;   // the largest value of a scaled row (of keys, queries) is below 2^kRowTop
 
 // What a row's values times 2^e have to be multiplied by to be x / sqrt(sum x^2 + eps), `sum` the sum of the scaled
-// squares.  One form keeps large rows from overflowing, the other rows far below eps from NaN.
+// squares.  One form keeps large rows from overflowing, the other rows far below eps, scaled, from eps = infinity.
 __device__ __forceinline__ float scaled_rsqrt(float sum, int e, float eps) {
     const float f = pow2(e), inv = pow2(-e);
-    return e <= 60 || eps == 0.f ? 1.f / sqrtf(sum + eps * f * f) : inv / sqrtf(sum * inv * inv + eps);
+    return e <= 0 || (e <= 60 && eps <= 1.f) || eps == 0.f ? 1.f / sqrtf(sum + eps * f * f) : inv / sqrtf(sum * inv * inv + eps);
 }
 
 // Whether sum x^2 (+ eps) may be used as it came out of FP32: no square has overflowed, and those that were flushed

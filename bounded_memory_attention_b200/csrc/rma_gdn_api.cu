@@ -54,6 +54,8 @@ int check_gdn_config(const rma_gdn_config* c) {
     if (c->qk_l2norm != 0 && c->qk_l2norm != 1) return api_fail(RMA_ERR_INVALID_ARG, "qk_l2norm must be 0 or 1");
     if (!(std::isfinite(c->l2_eps) && c->l2_eps >= 0.f))
         return api_fail(RMA_ERR_INVALID_ARG, "l2_eps must be finite and >= 0");
+    // (a key far below a larger eps, times a decay, would leave FP32's normal numbers)
+    if (c->l2_eps > 1e30f) return api_fail(RMA_ERR_UNSUPPORTED, "l2_eps > 1e30");
     if (!std::isfinite(c->scale)) return api_fail(RMA_ERR_INVALID_ARG, "scale must be finite");
     if ((int64_t)c->batch * c->n_v_heads > (1 << 22)) return api_fail(RMA_ERR_UNSUPPORTED, "batch * n_v_heads > 2^22");
     if ((2ll * c->n_k_heads + c->n_v_heads) * c->head_dim > (1 << 20))

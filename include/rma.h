@@ -377,7 +377,7 @@ typedef struct rma_gdn_config {
     int32_t head_dim;    /* 128 */
     int32_t conv_width;  /* taps of the short convolution (4) */
     int32_t qk_l2norm;   /* 1: q and k are divided by sqrt(sum x^2 + l2_eps) first; 0: taken as they are */
-    float   l2_eps;      /* >= 0 */
+    float   l2_eps;      /* 0 to 1e30 */
     float   scale;       /* of the output, 1/sqrt(head_dim) */
 } rma_gdn_config;
 

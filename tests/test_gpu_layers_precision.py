@@ -164,3 +164,23 @@ def test_how_far_back_a_chunk_is_spoilt(what):
         rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, st.workspace(n))
         fine = torch.isfinite(out.float()).flatten(2).all(-1)[0]
         assert fine[:first].all() and not fine[t:].any() and not torch.isfinite(st.delta).any()
+
+
+@pytest.mark.parametrize("n", [1, 5, 70])
+@pytest.mark.parametrize("eps", [3.0, 1e12, 1e30])
+@pytest.mark.parametrize("scale", [2.0 ** -56, 1.0, 2.0 ** 60])
+def test_rows_beside_a_large_eps(n, eps, scale):
+    """Any l2_eps that is not refused: rows far below it become x / sqrt(eps), tiny but not 0, in both forms."""
+    rma, _, _, x = delta_case(1, n, 1, 2, seed=350, fresh=True)
+    x["qkv"][..., :256] = (x["qkv"][..., :256].float() * scale).to(BF)
+    x["qkv"][..., 256:] = (x["qkv"][..., 256:].float() * 2.0 ** 60).to(BF)
+    d = {k: v.cuda() for k, v in x.items()}
+    st = rma.GdnState(rma.GdnConfig(n_k_heads=1, n_v_heads=2, l2_eps=eps))
+    out = torch.empty(1, n, 2, 128, dtype=BF, device="cuda")
+    if n == 1:
+        rma.gdn_decode_step(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out)
+    else:
+        rma.gdn_prefill(st, 0, d["qkv"], d["a"], d["b"], d["a_log"], d["dt_bias"], out, st.workspace(n))
+    _, S, _, size = delta_reference(x, 1, l2_eps=float(np.float32(eps)))
+    assert np.abs(S).max() > 2.0 ** -90   # not lost in FP32
+    assert (np.abs(f64(st.delta[0]) - S) <= 2.0 ** -15 * size.max((-1, -2), keepdims=True)).all()

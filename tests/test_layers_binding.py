@@ -21,6 +21,12 @@ def test_sizes_beyond_32_bits_are_refused_and_not_cut(rma, field, times):
         rma.gdn_state_bytes(cfg)
 
 
+def test_an_eps_beyond_its_range_is_refused(rma):
+    """Beside 3e38 a key of 2^-56 is normed to 2^-120, and with its decay it leaves FP32's normal numbers in a chunk."""
+    assert rma.gdn_state_bytes(rma.GdnConfig(l2_eps=3e38)) == 0 and "l2_eps" in rma.lib.rma_last_error().decode()
+    assert rma.gdn_state_bytes(rma.GdnConfig(l2_eps=1e30)) > 0
+
+
 @pytest.mark.parametrize("layer", [2 ** 32, 2 ** 31, -2 ** 32, 2 ** 63])
 def test_layers_beyond_32_bits_are_refused_and_not_cut(rma, layer):
     from bounded_memory_attention_b200 import layers
