@@ -655,9 +655,9 @@ __global__ void __launch_bounds__(kPrepThreads, 3) gdn_prep_kernel(const __grid_
 // ---------------------------------------------------------------------------
 // launch 2
 //
-// Bound by latency: the chunks of a head follow one another, 2.6 us each (4,900 cycles: the state's update and
+// Bound by latency: the chunks of a head follow one another, 2.5 us each (4,900 cycles: the state's update and
 // split 1,000, wait for W 500, X 680, wait for U 550, its splits 900, V and the increment 1,050), and a CTA starts and
-// ends in 8 us.  Measured on one B200: 335 us for 8,192 tokens of one sequence (32 CTAs), 37 us for 8 x 256
+// ends in 8 us.  Measured on one B200: 330 us for 8,192 tokens of one sequence (32 CTAs), 37 us for 8 x 256
 // (256 CTAs on 148 SMs).  What shortened the chain: products issued by one elected lane of a converged
 // warp (39 cycles an instruction; from a branch of one lane 103), scales from bounds that the first launch computes
 // instead of maxima over the chunk, outputs left to warps of their own, registers moved to the warps that hold the
@@ -793,19 +793,25 @@ __device__ __forceinline__ void lds4(const float* p, f2& a, f2& b) {
     b = v.y;
 }
 
-// ptx::mbar_wait_warp in less code, of which the scan has twenty copies: it gives up without setting the status, which is
-// set once, at the CTA's end (8,192 tokens of 32 heads: 354 us, 395 with the longer form; the instruction caches).
+// ptx::mbar_wait_warp in less code, of which the scan has twenty copies (8,192 tokens of 32 heads: 348 us, 395 with the
+// longer form; the instruction caches).  A wait that gives up raises the CTA's abort flag, which every store looks at, and
+// from which the status is set once, at the end.  kVerdict: false in all lanes if any has given up.  The clock's low word
+// wraps above the limit.
+template <bool kVerdict>
 __device__ __forceinline__ bool scan_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    const long long t0 = clock64();
+    static_assert(ptx::kWaitLimitCycles < 0xffffffffll, "measured by the clock's low word");
+    const uint32_t t0 = (uint32_t)clock();
     bool ok = true;
     while (!ptx::mbar_try_wait(bar, parity)) {
-        if (*abort || clock64() - t0 > ptx::kWaitLimitCycles) {
+        if (*abort || (uint32_t)clock() - t0 > (uint32_t)ptx::kWaitLimitCycles) {
             *abort = 1;
             ok = false;
             break;
         }
     }
-    return __all_sync(0xffffffffu, ok);
+    if constexpr (kVerdict) return __all_sync(0xffffffffu, ok);
+    __syncwarp();
+    return ok;
 }
 
 // Wait, bounded as the waits on barriers are, until another CTA has set the flag.  By a whole warp, with one verdict.
@@ -891,7 +897,6 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
     ptx::tc_fence_after();
     // all of tensor memory is this CTA's, so its first column is 0: the products' operands are then constants
     constexpr uint32_t tmem = 0;
-    bool ok = true;
 
     if (warp >= kWarpLoad) {
         regs_down<kRegsRest>();
@@ -902,9 +907,9 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             int issued = 0;
             for (int c = 0; c < nc; ++c) {
                 const int st = c % kStages;
-                if (c >= kStages && !scan_wait(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag)) break;
+                if (c >= kStages && !scan_wait<true>(&bars[kbEmpty + st], (c / kStages - 1) & 1, abort_flag)) break;
                 // the state and the first chunk come first: they are what the start waits for
-                if (c == 1 && !scan_wait(&bars[kbS], 0, abort_flag)) break;
+                if (c == 1 && !scan_wait<true>(&bars[kbS], 0, abort_flag)) break;
                 if (ready && !item_ready(ready + ((int64_t)c * a.B + b) * a.HK + kh, abort_flag)) break;
                 issued = c + 1;
                 uint8_t* stage = smem + st * kStageBytes;
@@ -938,7 +943,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 // columns).  16 values of the rows of an image are 32 bytes: 2 in the address field
                 const uint32_t dk = (kb >> 4) | (1u << 16), dt = (tb >> 4) | (1u << 16), dd = (kb >> 4) | ((uint32_t)(kTile >> 4) << 16);
                 auto wait = [&](int bar, int phase) {
-                    const bool there = scan_wait(&bars[bar], phase & 1, abort_flag);
+                    const bool there = scan_wait<true>(&bars[bar], phase & 1, abort_flag);
                     ptx::tc_fence_after();
                     return there;
                 };
@@ -1025,10 +1030,10 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             uint8_t* stage = smem + st * kStageBytes;
             const float* scal = reinterpret_cast<const float*>(stage + kStageTP + kOffScal);
             const int left = len - c * kC;
-            ok = scan_wait(&bars[kbFull + st], (c / kStages) & 1, abort_flag) && ok;
-            ok = scan_wait(&bars[kbU], c & 1, abort_flag) && ok;   // the scales
+            scan_wait<false>(&bars[kbFull + st], (c / kStages) & 1, abort_flag);
+            scan_wait<false>(&bars[kbU], c & 1, abort_flag);   // the scales
             const float inv_p = scal[kPS];
-            ok = scan_wait(&bars[kbPDone], c & 1, abort_flag) && ok;
+            scan_wait<false>(&bars[kbPDone], c & 1, abort_flag);
             ptx::tc_fence_after();
 #pragma unroll 1
             for (int hl = 0; hl < 2; ++hl) {            // 16 columns
@@ -1076,9 +1081,8 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             }
             ptx::fence_proxy_async_smem();
             ptx::named_bar_sync(kBarOut, 128);
-            ok = ok && *abort_flag == 0;   // a wait that gave up in another of these warps, too
-            if (!ok) {
-                // an abandoned CTA: what stands in the stage is nobody's output
+            if (*abort_flag) {
+                // a wait has given up: what stands in the stage is nobody's output
             } else if (left >= kC) {
                 if (warp == kWarpOut && lane < 2) {
                     tma_store_2d(&maps.out, stage + kStageV + lane * kTile, h * kGdnDim + 64 * lane, b * a.n + c * kC);
@@ -1172,7 +1176,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             const float* one = reinterpret_cast<const float*>(smem + st * kStageBytes + kStageTP + kOffScal);
             const float* scal = one + 32 * wg;   // this half's tokens
             // while W is computed: the bounds and the scales
-            ok = scan_wait(&bars[kbS + (wg ^ 1)], c & 1, abort_flag) && ok;
+            scan_wait<false>(&bars[kbS + (wg ^ 1)], c & 1, abort_flag);
             take(smax, vmax);
             const float inv_s = pow2(-es);
             smax *= inv_s;
@@ -1192,7 +1196,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
             }
             // X
             // (an abandoned CTA goes on through its barriers, on values that nobody uses)
-            ok = scan_wait(&bars[kbWDone], c & 1, abort_flag) && ok;
+            scan_wait<false>(&bars[kbWDone], c & 1, abort_flag);
             ptx::tc_fence_after();
             ptx::tmem_ld32(tl + kTmW + 32 * wg, x);
             ptx::tmem_wait_ld();
@@ -1212,7 +1216,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 signal(kbX);
             }
             // U, and U scaled for the state
-            ok = scan_wait(&bars[kbUDone + wg], c & 1, abort_flag) && ok;
+            scan_wait<false>(&bars[kbUDone + wg], c & 1, abort_flag);
             ptx::tc_fence_after();
             {
                 const f2 cu2 = pack2(cu, cu), cd2 = pack2(cd, cd);
@@ -1250,12 +1254,12 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
           }
             // while the increment is computed: the next chunk's V
             if (c + 1 < nc) {
-                ok = scan_wait(&bars[kbFull + (c + 1) % kStages], ((c + 1) / kStages) & 1, abort_flag) && ok;
+                scan_wait<false>(&bars[kbFull + (c + 1) % kStages], ((c + 1) / kStages) & 1, abort_flag);
                 vmax = get_v(c + 1);
             }
             // the state
             if (c >= 0) {
-                ok = scan_wait(&bars[kbDDone], c & 1, abort_flag) && ok;
+                scan_wait<false>(&bars[kbDDone], c & 1, abort_flag);
                 ptx::tc_fence_after();
                 es = es1;
                 const f2 k2 = pack2(ck, ck);
@@ -1286,7 +1290,7 @@ __device__ __forceinline__ void scan_head(const DeltaArgs& a, const ScanMaps& ma
                 signal(kbS);
             }
         }
-        if (ok) {
+        if (*abort_flag == 0) {   // no wait of this CTA has given up
             const float f = pow2(-es);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -1313,8 +1317,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) gdn_scan_kernel(const __grid_
 // items at a time of launch 1, chunk by chunk.  A finished item sets its flag, and a head's loads wait for it.  The
 // launch is cooperative, so that all CTAs are there, and those that are waited for do not wait themselves.
 //
-// Measured on one B200, 16 key and 32 value heads: 355 us for 8,192 tokens (424 in two launches), 108 (116) for 2,048;
-// two sequences of 4,096 tokens 206 (260).
+// Measured on one B200, 16 key and 32 value heads: 348 us for 8,192 tokens (419 in two launches), 107 (115) for 2,048;
+// two sequences of 4,096 tokens 206 (257).
 // ---------------------------------------------------------------------------
 constexpr int kPrepSlot = (sizeof(PrepSmem) + 1023) / 1024 * 1024;
 static_assert(2 * kPrepThreads == kScanThreads && 2 * kPrepSlot + 1024 <= kScanSmem, "two items in a CTA of the scan's size");
@@ -1370,7 +1374,7 @@ size_t gdn_prefill_workspace_bytes(const rma_gdn_config& c, int n) {
 }
 
 // Heads on at most half of the multiprocessors, 32 chunks or more, and the others keep ahead of the heads: an item
-// with two value heads takes 12 us, two items at a time a CTA, a chunk of the scan 2.6 us.  And more items than launch 1
+// with two value heads takes 12 us, two items at a time a CTA, a chunk of the scan 2.5 us.  And more items than launch 1
 // runs at once, three an SM, since with fewer it is over in the time of one: 2,048 tokens of 8 and 16 heads (256 items)
 // 104 us here, 100 in two launches, 8,192 of 2 and 4 (256) 344 and 342; 2,048 of 16 and 16 (512) 102 and 108, 8,192 of 4
 // and 4 (512) 342 and 352.

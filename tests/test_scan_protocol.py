@@ -38,14 +38,14 @@ def test_the_kernel_hands_over_with_the_state():
     """The scan arrives on no named barrier without waiting there, and a half waits for the other's state, bounded."""
     src = open(SOURCE).read()
     assert "named_bar_arrive" not in src
-    assert "scan_wait(&bars[kbS + (wg ^ 1)], c & 1, abort_flag)" in src
+    assert "scan_wait<false>(&bars[kbS + (wg ^ 1)], c & 1, abort_flag)" in src
 
 
 def test_an_abandoned_cta_stores_no_outputs():
-    """Every store of the output warps, and of the state, stands behind the verdict of the waits before it."""
+    """Every store of the output warps, and of the state, stands behind a look at the abort flag after the waits before it."""
     src = open(SOURCE).read()
     out = src[src.index("ptx::named_bar_sync(kBarOut, 128)"):src.index("ptx::mbar_arrive(&bars[kbEmpty + st])")]
-    guard = out.index("if (!ok)")
-    assert out.index("*abort_flag") < guard < out.index("} else if (left >= kC) {") < out.index("tma_store_2d")
-    last = src[src.rindex("if (ok) {"):]
-    assert last.index("gs[2 * i * kGdnDim] =") < last.index("__syncthreads")
+    assert out.index("if (*abort_flag) {") < out.index("} else if (left >= kC) {") < out.index("tma_store_2d")
+    last = src[src.rindex("if (*abort_flag == 0) {"):]
+    assert "scan_wait" not in last[:last.index("gs[2 * i * kGdnDim] =")] and last.index("gs[2 * i * kGdnDim] =") < last.index("__syncthreads")
+    assert src.count("gs[2 * i * kGdnDim] =") == 1 and src.count("tma_store_2d(&maps.out") == 1
